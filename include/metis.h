@@ -22,7 +22,7 @@
  *     host-side validation and launch only; numeric failures found on the device
  *     latch bits of the status word (METIS_DEV_*), read by
  *     metis_poll_device_status.  No kernel traps.
- *   - Shapes: every matrix dimension is a multiple of 128 (and, where it is a GeMM
+ *   - Shapes (where a call does not say otherwise): every matrix dimension is a multiple of 128 (and, where it is a GeMM
  *     contraction length, of 256); 1 <= k <= 64; k + s <= 128; k + s <= l_k <= rows.
  *   - Alignment: pointers 16-byte aligned; bf16 leading dimensions a multiple of 8
  *     elements, fp32 ones a multiple of 4.
@@ -331,6 +331,110 @@ metis_status metis_lora_constrain(metis_ctx* ctx, float* L2, int64_t m, float* L
 metis_status metis_lora_realign(metis_ctx* ctx, float* W_res, int64_t m, int64_t n, int64_t ldw, float* L2,
                                 float* L1, int32_t k, float beta, const metis_decomp_params* p, uint32_t step,
                                 metis_factors* f, void* W_bf16);
+
+/*
+ * 8-bit integer tensor in one orientation: outer x inner signed codes, row-major with
+ * leading dimension ld (bytes), and one fp32 scale for each of the outer lines:
+ * decoded value = codes[o * ld + i] * scales[o].  inner is the contraction dimension of
+ * the product that reads it.  codes 16-byte aligned, ld >= inner and a multiple of 16;
+ * the bytes from inner to ld of a line are neither read nor written.  Unlike the NVFP4
+ * operands these have no limits on outer and inner besides 1 <= outer, inner < 2^31.
+ */
+typedef struct {
+  int8_t* codes;
+  float* scales;
+  int64_t outer, inner, ld;
+} metis_int8;
+
+/*
+ * 8-bit quantization of a device matrix M (rows x cols, leading dimension ld >= cols,
+ * dtype METIS_OUT_F32 or METIS_OUT_BF16, aligned to its element), round to nearest:
+ *   rowwise (nullable): outer = rows, inner = cols, a scale for each row (token)
+ *   colwise (nullable): outer = cols, inner = rows, a scale for each column (channel); M^T
+ * For a line with amax = max |x| over its finite entries and a = max(amax, 127 * 2^-126):
+ * scale = fp32(a / 127), code = 127 x / a rounded to the nearest integer, ties to even,
+ * decided on the exact quotient.  A line of zeros has zero codes.  NaN gives code 0, an
+ * infinity +-127; device: METIS_DEV_NONFINITE for both.  No workspace.
+ */
+metis_status metis_quantize_int8(metis_ctx* ctx, const void* M, int64_t rows, int64_t cols, int64_t ld, int32_t dtype,
+                                 metis_int8* rowwise, metis_int8* colwise);
+
+/*
+ * Product of 8-bit integer tensors with a scale for each line of both:
+ *   C[i][j] = (sum_k A(i,k) B(j,k)) * A.scales[i] * B.scales[j]
+ * for A (p x K) and B (q x K), A.inner == B.inner = K <= 131071, C p x q with leading
+ * dimension ldc and type c_dtype (METIS_OUT_*).  The sum is exact in int32 for all codes
+ * (-128 too); it is converted to fp32 (nearest), multiplied by A.scales[i], then by
+ * B.scales[j], and rounded to c_dtype.  C is 16-byte aligned with ldc a multiple of 16
+ * bytes; its columns from q to ldc are not written.  No workspace.
+ * Errors: ERR_ARG, ERR_SHAPE, ERR_ALIGN.  Device: METIS_DEV_TIMEOUT.
+ */
+metis_status metis_gemm_int8(metis_ctx* ctx, const metis_int8* A, const metis_int8* B, void* C, int64_t ldc,
+                             int32_t c_dtype);
+
+/*
+ * Linear layer on held 8-bit weights: quantizes X (p x K, as metis_quantize_int8 row-wise)
+ * into Xq (p x K, caller-owned, written) and computes C = Xq W^T as metis_gemm_int8 with
+ * W (q x K, a scale for each output channel).
+ */
+metis_status metis_linear_int8(metis_ctx* ctx, const void* X, int64_t ld, int32_t dtype, metis_int8* Xq,
+                               const metis_int8* W, void* C, int64_t ldc, int32_t c_dtype);
+
+/*
+ * One AdamW step over many tensors:
+ *   m = b1 m + (1 - b1) g,   v = b2 v + (1 - b2) g^2,
+ *   p = p (1 - lr wd) - lr / (1 - b1^t) * m / (sqrt(v) / sqrt(1 - b2^t) + eps)
+ * p and g: n contiguous elements of one type (dtype METIS_OUT_F32 or METIS_OUT_BF16).
+ * state_bits 32: m and v fp32.  state_bits 8: m and v one byte an element, and one
+ * exponent byte E for each block of 128 consecutive elements (ceil(n / 128) bytes each in
+ * m_exponent and v_exponent), E = 127 + floor(log2(largest magnitude of the block)), at
+ * least 16 (2^-111) and at most 254.  Codes are small floats with 3 mantissa bits and
+ * gradual underflow:
+ *   m: bit 7 the sign, c = bits 0-6, u = 2^(E - 144);   v: c = bits 0-7, u = 2^(E - 160)
+ *   value = c u for c < 8, else (8 + c % 8) 2^(c / 8 - 1) u
+ * Values beyond the largest code (within the block's top octave) take it; a positive v
+ * takes code 1 at least.  All zero bytes are a fresh state.  8-bit moments are computed in
+ * fp64, in the order b1 m + (1 - b1) g and b2 v + (1 - b2) (g g), each operation rounded;
+ * the parameter (fp32 arithmetic) is updated with them before they become codes.
+ * rounding 0: codes and bf16 parameters to nearest, ties to even; 1: stochastic, with
+ * Philox words of key seed and counter (e / 4 lo, hi, id << 8 | 4 << 4 | sub, t) for
+ * element e of the tensor, word e % 4: a code is floor(x + (r + 1/2) 2^-16) in units of its
+ * grid step, r the low 16 bits of the sub 0 word for m and the high 16 bits for v; a bf16
+ * parameter is its fp32 value's upper half after adding the low 16 bits of the sub 1 word.
+ * Fp32 parameters and 32-bit states are not rounded further.
+ * id (< 2^24) separates the random streams of the tensors.  t = step >= 1, or *step_dev
+ * (device, read when the kernel runs) when step_dev is given; lr, or *lr_dev likewise, so a
+ * captured graph can step on.  Tensors with n == 0 are skipped; count may be 0.  The arrays
+ * of the tensors must not overlap.  `tensors` is read during the call.  No workspace.
+ * A gradient that is NaN or infinite raises METIS_DEV_NONFINITE and makes its element's
+ * parameter NaN, as in the formula; 8-bit states of that element become zero.
+ * Errors: ERR_ARG for null arrays, a bad enum, b1 or b2 outside [0, 1), eps < 0, step < 1,
+ * a non-finite coefficient or id >= 2^24; ERR_ALIGN for an array not aligned to its element.
+ */
+typedef struct {
+  void* p;
+  const void* g;
+  void* m;
+  void* v;
+  uint8_t* m_exponent;
+  uint8_t* v_exponent;
+  int64_t n;
+  int32_t dtype;
+  uint32_t id;
+} metis_adamw_tensor;
+
+typedef struct {
+  double lr, beta1, beta2, eps, weight_decay;
+  int64_t step;
+  int32_t state_bits;
+  int32_t rounding;
+  uint64_t seed;
+  const float* lr_dev;
+  const int64_t* step_dev;
+} metis_adamw_params;
+
+metis_status metis_adamw_step(metis_ctx* ctx, const metis_adamw_tensor* tensors, int64_t count,
+                              const metis_adamw_params* q);
 
 /*
  * Self-test of failure detection (no counterpart in the notes).  Every wait of the

@@ -27,9 +27,11 @@ Modules, in the order the method uses them:
                    ("Full-Stack FP4" technical summary, section 2.1): the branch
                    product, its gradients, the Cholesky-QR constraint and the
                    randomized-SVD realignment.
+* ``int8``      -- 8-bit integer quantizer (a scale for each line) and the product of its codes.
+* ``adamw``     -- AdamW with fp32 or 8-bit moments (small floats under a shared exponent).
 
 Parity status of every function is listed in its module header.  Nothing in
 this package is "parity unpinned" except where a header says so explicitly.
 """
 
-from . import philox, formats, nvfp4, linalg, decompose, metis, lora_svd  # noqa: F401
+from . import philox, formats, nvfp4, linalg, decompose, metis, lora_svd, int8, adamw  # noqa: F401

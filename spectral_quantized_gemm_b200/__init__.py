@@ -36,6 +36,7 @@ STATUS_NAMES = {0: "OK", 1: "ERR_ARG", 2: "ERR_SHAPE", 3: "ERR_ALIGN", 4: "ERR_A
                 6: "ERR_WORKSPACE"}
 DEV_NUMERIC, DEV_NONFINITE, DEV_TIMEOUT = 1, 2, 4
 OUT_F32, OUT_BF16 = 0, 1
+_DTYPES = {torch.float32: OUT_F32, torch.bfloat16: OUT_BF16}
 
 EXPORTED = ["metis_create", "metis_destroy", "metis_set_stream", "metis_status_str", "metis_last_error",
             "metis_poll_device_status", "metis_nvfp4_codes_bytes", "metis_nvfp4_scales_bytes",
@@ -45,7 +46,8 @@ EXPORTED = ["metis_create", "metis_destroy", "metis_set_stream", "metis_status_s
             "metis_nvfp4_mma_peak", "metis_selftest_wait_timeout", "metis_lora_linear",
             "metis_lora_branch_grad", "metis_lora_constrain", "metis_lora_realign",
             "metis_residual_quantize_nvfp4_dump", "metis_profile_read_kind", "metis_set_sm_count_target",
-            "metis_selftest_numeric"]
+            "metis_selftest_numeric", "metis_quantize_int8", "metis_gemm_int8", "metis_linear_int8",
+            "metis_adamw_step"]
 
 PROF_GEMM, PROF_RESQUANT, PROF_PROJECTION = 0, 1, 2
 
@@ -71,6 +73,21 @@ class DecompParams(ctypes.Structure):
 class QuantParams(ctypes.Structure):
     _fields_ = [("rounding", c_i32), ("seed", c_u64), ("operand_id", c_u32), ("step", c_u32),
                 ("tensor_scale", c_f32)]
+
+
+class Int8Struct(ctypes.Structure):
+    _fields_ = [("codes", c_p), ("scales", c_p), ("outer", c_i64), ("inner", c_i64), ("ld", c_i64)]
+
+
+class AdamWTensor(ctypes.Structure):
+    _fields_ = [("p", c_p), ("g", c_p), ("m", c_p), ("v", c_p), ("m_exponent", c_p), ("v_exponent", c_p), ("n", c_i64),
+                ("dtype", c_i32), ("id", c_u32)]
+
+
+class AdamWParams(ctypes.Structure):
+    _fields_ = [("lr", ctypes.c_double), ("beta1", ctypes.c_double), ("beta2", ctypes.c_double),
+                ("eps", ctypes.c_double), ("weight_decay", ctypes.c_double), ("step", c_i64), ("state_bits", c_i32),
+                ("rounding", c_i32), ("seed", c_u64), ("lr_dev", c_p), ("step_dev", c_p)]
 
 
 class OperandStruct(ctypes.Structure):
@@ -122,6 +139,12 @@ _lora_grad = _sig("metis_lora_branch_grad", c_i32, c_p, ctypes.POINTER(Matrix), 
 _lora_constrain = _sig("metis_lora_constrain", c_i32, c_p, c_p, c_i64, c_p, c_i64, c_i32)
 _lora_realign = _sig("metis_lora_realign", c_i32, c_p, c_p, c_i64, c_i64, c_i64, c_p, c_p, c_i32, c_f32,
                      ctypes.POINTER(DecompParams), c_u32, ctypes.POINTER(FactorsStruct), c_p)
+_quant_i8 = _sig("metis_quantize_int8", c_i32, c_p, c_p, c_i64, c_i64, c_i64, c_i32, ctypes.POINTER(Int8Struct),
+                 ctypes.POINTER(Int8Struct))
+_gemm_i8 = _sig("metis_gemm_int8", c_i32, c_p, ctypes.POINTER(Int8Struct), ctypes.POINTER(Int8Struct), c_p, c_i64, c_i32)
+_linear_i8 = _sig("metis_linear_int8", c_i32, c_p, c_p, c_i64, c_i32, ctypes.POINTER(Int8Struct),
+                  ctypes.POINTER(Int8Struct), c_p, c_i64, c_i32)
+_adamw = _sig("metis_adamw_step", c_i32, c_p, c_p, c_i64, ctypes.POINTER(AdamWParams))
 
 _launches = _sig("metis_kernel_launches", c_u64)
 _prof_enable = _sig("metis_profile_enable", c_i32, c_p, ctypes.c_int)
@@ -178,6 +201,53 @@ class Factors:
                                     self.S.data_ptr(), self.Uq.struct, self.Vq.struct,
                                     None if self.sampled_rows is None else self.sampled_rows.data_ptr(),
                                     None if self.omega is None else self.omega.data_ptr())
+
+
+class Int8:
+    """8-bit integer tensor in one orientation: codes (outer x inner, int8) and one fp32 scale
+    for each of the outer lines (decoded value = codes[o, i] * scales[o]); inner is the
+    contraction dimension of the product that reads it.
+
+    codes / scales: existing CUDA tensors to use instead of new ones -- codes a row-major
+    view whose row stride is a multiple of 16 and whose first element is 16-byte aligned."""
+
+    def __init__(self, outer, inner, device="cuda", codes=None, scales=None):
+        self.outer, self.inner = int(outer), int(inner)
+        if self.outer < 1 or self.inner < 1:
+            raise ValueError("outer and inner must be at least 1")
+        if codes is None:
+            codes = torch.empty(self.outer, -(-self.inner // 16) * 16, dtype=torch.int8, device=device)[:, :self.inner]
+        if scales is None:
+            scales = torch.empty(self.outer, dtype=torch.float32, device=codes.device)
+        if codes.dtype != torch.int8 or codes.shape != (self.outer, self.inner) or \
+                (codes.stride(1) != 1 and self.inner > 1):
+            raise ValueError("codes: expected a row-major int8 CUDA tensor of outer x inner")
+        if scales.dtype != torch.float32 or scales.shape != (self.outer,) or (scales.stride(0) != 1 and self.outer > 1):
+            raise ValueError("scales: expected a contiguous fp32 CUDA tensor of outer elements")
+        if not codes.is_cuda or scales.device != codes.device:
+            raise ValueError("codes and scales must be on the same CUDA device")
+        # the row stride of a single row says nothing and may be anything
+        ld = codes.stride(0) if self.outer > 1 else -(-self.inner // 16) * 16
+        self.codes, self.scales = codes, scales
+        self.struct = Int8Struct(codes.data_ptr(), scales.data_ptr(), self.outer, self.inner, ld)
+
+    def dequantize(self):
+        """The decoded fp32 matrix (outer x inner)."""
+        return self.codes.float() * self.scales[:, None]
+
+
+def _dense(M, name):
+    """(pointer, leading dimension, dtype) of a row-major 2-D fp32 or bf16 CUDA tensor."""
+    dtype = _DTYPES.get(M.dtype)
+    if dtype is None or M.dim() != 2 or not M.is_cuda or (M.stride(1) != 1 and M.shape[1] > 1):
+        raise ValueError(f"{name}: expected a row-major 2-D fp32 or bf16 CUDA tensor")
+    rows, cols = M.shape
+    ld = M.stride(0)
+    if rows == 1:          # the stride of a single row says nothing
+        ld = -(-cols // 8) * 8
+    if ld < cols:
+        raise ValueError(f"{name}: rows overlap")
+    return M.data_ptr(), ld, dtype
 
 
 def _matrix(M):
@@ -337,6 +407,56 @@ class Context:
     def linear_fwd(self, X, W, Y):
         dtype = OUT_F32 if Y.dtype == torch.float32 else OUT_BF16
         self._call(_fwd, ctypes.byref(X), ctypes.byref(W), _ptr(Y), Y.stride(0), dtype)
+
+    # -- 8-bit integer layer ------------------------------------------------------
+    def new_int8(self, outer, inner):
+        return Int8(outer, inner, self.device)
+
+    def _same_device(self, **tensors):
+        for name, t in tensors.items():
+            t = t.codes if isinstance(t, Int8) else t
+            if t is not None and t.device != self.device:
+                raise ValueError(f"{name} is on {t.device}, the context on {self.device}")
+
+    def quantize_int8(self, M, rowwise=None, colwise=None):
+        """8-bit codes and scales of the rows of M (fp32 or bf16) into `rowwise` (rows x cols)
+        and / or of its columns into `colwise` (cols x rows)."""
+        self._same_device(M=M, rowwise=rowwise, colwise=colwise)
+        ptr, ld, dtype = _dense(M, "M")
+        self._call(_quant_i8, ptr, M.shape[0], M.shape[1], ld, dtype,
+                   None if rowwise is None else ctypes.byref(rowwise.struct),
+                   None if colwise is None else ctypes.byref(colwise.struct))
+
+    def gemm_int8(self, A, B, C):
+        """C[i, j] = (sum_k A[i, k] B[j, k]) A.scales[i] B.scales[j] (C fp32 or bf16)."""
+        self._same_device(A=A, B=B, C=C)
+        ptr, ld, dtype = _dense(C, "C")
+        if C.shape != (A.outer, B.outer):
+            raise ValueError(f"C: expected {A.outer} x {B.outer}, got {tuple(C.shape)}")
+        self._call(_gemm_i8, ctypes.byref(A.struct), ctypes.byref(B.struct), ptr, ld, dtype)
+
+    def linear_int8(self, X, Xq, W, Y):
+        """Y = Q(X) W^T for held 8-bit weights W (out x in): X (tokens x in, fp32 or bf16) is
+        quantized by rows into the buffer Xq on the way."""
+        self._same_device(X=X, Xq=Xq, W=W, Y=Y)
+        ptr, ld, dtype = _dense(X, "X")
+        yptr, ldy, ydtype = _dense(Y, "Y")
+        if X.shape != (Xq.outer, Xq.inner) or Y.shape != (Xq.outer, W.outer):
+            raise ValueError("expected X like Xq (tokens x in) and Y of tokens x out")
+        self._call(_linear_i8, ptr, ld, dtype, ctypes.byref(Xq.struct), ctypes.byref(W.struct), yptr, ldy, ydtype)
+
+    # -- optimizer step -----------------------------------------------------------
+    def adamw_step(self, tensors, count, lr, beta1, beta2, eps, weight_decay, step, state_bits=32, rounding=0, seed=0,
+                   lr_dev=None, step_dev=None):
+        """One AdamW step over `count` entries of `tensors` (an array of AdamWTensor, or its
+        address); lr_dev (fp32) and step_dev (int64) are one-element CUDA tensors that, when
+        given, replace lr and step.  spectral_quantized_gemm_b200.optim.AdamW builds the entries."""
+        for t, dtype, name in ((lr_dev, torch.float32, "lr_dev"), (step_dev, torch.int64, "step_dev")):
+            if t is not None and (t.dtype != dtype or t.numel() != 1 or t.device != self.device):
+                raise ValueError(f"{name}: expected one {dtype} element on {self.device}")
+        q = AdamWParams(lr, beta1, beta2, eps, weight_decay, step, state_bits, rounding, seed & (2 ** 64 - 1),
+                        None if lr_dev is None else lr_dev.data_ptr(), None if step_dev is None else step_dev.data_ptr())
+        self._call(_adamw, tensors, count, ctypes.byref(q))
 
     # -- LoRA-SVD linear projection (W = W_res + beta L2 L1) --------------------
     @staticmethod

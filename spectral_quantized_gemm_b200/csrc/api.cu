@@ -5,6 +5,7 @@
 
 #include <cmath>
 #include <cstring>
+#include <exception>
 #include <new>
 #include <string>
 
@@ -133,19 +134,22 @@ extern "C" {
 metis_status metis_create(int device, void* stream, metis_ctx** out) {
   if (!out) return METIS_ERR_ARG;
   *out = nullptr;
-  cudaDeviceProp prop;
-  if (cudaGetDeviceProperties(&prop, device) != cudaSuccess) {
+  // single attributes: the whole property record takes milliseconds to collect
+  int major = 0, minor = 0, sms = 0;
+  if (cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, device) != cudaSuccess ||
+      cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, device) != cudaSuccess ||
+      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, device) != cudaSuccess) {
     cudaGetLastError();
     return METIS_ERR_CUDA;
   }
-  if (prop.major != 10 || prop.minor != 0) return METIS_ERR_ARCH;
+  if (major != 10 || minor != 0) return METIS_ERR_ARCH;
   if (cudaSetDevice(device) != cudaSuccess) return METIS_ERR_CUDA;
   metis_ctx* ctx = new (std::nothrow) metis_ctx();
   if (!ctx) return METIS_ERR_WORKSPACE;
   ctx->device = device;
   ctx->stream = static_cast<cudaStream_t>(stream);
-  ctx->sm_count = prop.multiProcessorCount;
-  ctx->sm_count_device = prop.multiProcessorCount;
+  ctx->sm_count = sms;
+  ctx->sm_count_device = sms;
   if (cudaMalloc(&ctx->status, sizeof(uint32_t)) != cudaSuccess || cudaMemset(ctx->status, 0, sizeof(uint32_t)) != cudaSuccess) {
     delete ctx;
     return METIS_ERR_CUDA;
@@ -561,3 +565,164 @@ extern "C" metis_status metis_residual_quantize_nvfp4_noalloc(metis_ctx* ctx, co
   return run_residual_quantize_into(ctx, M, f, q, rowwise, colwise, scratch,
                                     reinterpret_cast<uint32_t*>(scratch + kNoAllocAmaxOffset), nullptr, 0);
 }
+
+// ---- 8-bit integer layer and optimizer step ---------------------------------------
+namespace metis {
+namespace {
+
+// Enters the context's device for one call and leaves the caller's device current.
+struct DeviceScope {
+  int before = -1;
+  DeviceScope() {
+    if (cudaGetDevice(&before) != cudaSuccess) before = -1;
+  }
+  ~DeviceScope() {
+    if (before >= 0) cudaSetDevice(before);
+  }
+  DeviceScope(const DeviceScope&) = delete;
+  DeviceScope& operator=(const DeviceScope&) = delete;
+};
+
+// Runs the body of a C entry point; no C++ exception leaves it.
+template <typename F>
+metis_status guarded(metis_ctx* ctx, F&& body) {
+  if (!ctx) return METIS_ERR_ARG;
+  try {
+    const DeviceScope scope;
+    const metis_status s = enter(ctx);
+    return s == METIS_OK ? body() : s;
+  } catch (const std::exception&) {
+    return METIS_ERR_WORKSPACE;   // host memory
+  }
+}
+
+constexpr int64_t kMaxLine = INT32_MAX;
+
+metis_status check_dense(metis_ctx* ctx, const void* M, int64_t rows, int64_t cols, int64_t ld, int32_t dtype) {
+  if (!M) return fail(ctx, METIS_ERR_ARG, "null matrix");
+  if (dtype != METIS_OUT_F32 && dtype != METIS_OUT_BF16) return fail(ctx, METIS_ERR_ARG, "bad matrix dtype");
+  if (rows < 1 || cols < 1 || rows > kMaxLine || cols > kMaxLine)
+    return fail(ctx, METIS_ERR_SHAPE, "matrix dimensions must be in [1, 2^31)");
+  if (ld < cols) return fail(ctx, METIS_ERR_SHAPE, "leading dimension below the row length");
+  if (reinterpret_cast<uintptr_t>(M) & (dtype == METIS_OUT_F32 ? 3u : 1u))
+    return fail(ctx, METIS_ERR_ALIGN, "matrix not aligned to its element");
+  return METIS_OK;
+}
+
+metis_status check_int8(metis_ctx* ctx, const metis_int8* t, const char* name) {
+  if (!t->codes || !t->scales) return fail(ctx, METIS_ERR_ARG, std::string(name) + ": null codes or scales");
+  if (t->outer < 1 || t->inner < 1 || t->outer > kMaxLine || t->inner > kMaxLine)
+    return fail(ctx, METIS_ERR_SHAPE, std::string(name) + ": outer and inner must be in [1, 2^31)");
+  if (t->ld < t->inner || t->ld % 16 || !aligned16(t->codes))
+    return fail(ctx, METIS_ERR_ALIGN, std::string(name) + ": codes need 16-byte alignment, ld >= inner and ld % 16 == 0");
+  if (reinterpret_cast<uintptr_t>(t->scales) & 3u)
+    return fail(ctx, METIS_ERR_ALIGN, std::string(name) + ": scales must be 4-byte aligned");
+  return METIS_OK;
+}
+
+metis_status check_quantize_int8(metis_ctx* ctx, const void* M, int64_t rows, int64_t cols, int64_t ld, int32_t dtype,
+                                 const metis_int8* rowwise, const metis_int8* colwise) {
+  metis_status s;
+  if (!rowwise && !colwise) return fail(ctx, METIS_ERR_ARG, "no output orientation requested");
+  if ((s = check_dense(ctx, M, rows, cols, ld, dtype)) != METIS_OK) return s;
+  if (rowwise && (s = check_int8(ctx, rowwise, "rowwise")) != METIS_OK) return s;
+  if (colwise && (s = check_int8(ctx, colwise, "colwise")) != METIS_OK) return s;
+  if (rowwise && (rowwise->outer != rows || rowwise->inner != cols))
+    return fail(ctx, METIS_ERR_SHAPE, "rowwise: expected outer x inner = rows x cols");
+  if (colwise && (colwise->outer != cols || colwise->inner != rows))
+    return fail(ctx, METIS_ERR_SHAPE, "colwise: expected outer x inner = cols x rows");
+  return METIS_OK;
+}
+
+metis_status check_gemm_int8(metis_ctx* ctx, const metis_int8* A, const metis_int8* B, const void* C, int64_t ldc,
+                             int32_t c_dtype) {
+  metis_status s;
+  if (!A || !B || !C) return fail(ctx, METIS_ERR_ARG, "null operand");
+  if ((s = check_int8(ctx, A, "A")) != METIS_OK) return s;
+  if ((s = check_int8(ctx, B, "B")) != METIS_OK) return s;
+  if (A->inner != B->inner) return fail(ctx, METIS_ERR_SHAPE, "A.inner must equal B.inner");
+  if (A->inner > 131071) return fail(ctx, METIS_ERR_SHAPE, "K must not exceed 131071 (the int32 sum is exact below that)");
+  if (c_dtype != METIS_OUT_F32 && c_dtype != METIS_OUT_BF16) return fail(ctx, METIS_ERR_ARG, "bad output dtype");
+  if (ldc < B->outer || ldc % (c_dtype == METIS_OUT_F32 ? 4 : 8) || !aligned16(C))
+    return fail(ctx, METIS_ERR_ALIGN, "output needs 16-byte alignment and a 16-byte multiple leading dimension");
+  return METIS_OK;
+}
+
+metis_status check_adamw(metis_ctx* ctx, const metis_adamw_tensor* tensors, int64_t count, const metis_adamw_params* q) {
+  if (!q || count < 0 || (count > 0 && !tensors)) return fail(ctx, METIS_ERR_ARG, "null parameters or tensors");
+  if (q->state_bits != 8 && q->state_bits != 32) return fail(ctx, METIS_ERR_ARG, "state_bits must be 8 or 32");
+  if (q->rounding != 0 && q->rounding != 1) return fail(ctx, METIS_ERR_ARG, "rounding must be 0 (RN) or 1 (SR)");
+  if (!(q->beta1 >= 0.0 && q->beta1 < 1.0 && q->beta2 >= 0.0 && q->beta2 < 1.0))
+    return fail(ctx, METIS_ERR_ARG, "beta1 and beta2 must be in [0, 1)");
+  if (!(q->eps >= 0.0) || !std::isfinite(q->eps) || !std::isfinite(q->weight_decay) || !std::isfinite(q->lr))
+    return fail(ctx, METIS_ERR_ARG, "lr, eps and weight_decay must be finite, eps not negative");
+  if (!q->step_dev && q->step < 1) return fail(ctx, METIS_ERR_ARG, "step must be at least 1");
+  if ((reinterpret_cast<uintptr_t>(q->lr_dev) & 3u) || (reinterpret_cast<uintptr_t>(q->step_dev) & 7u))
+    return fail(ctx, METIS_ERR_ALIGN, "lr_dev and step_dev must be aligned to their elements");
+  for (int64_t i = 0; i < count; ++i) {
+    const metis_adamw_tensor& t = tensors[i];
+    const auto at = [i](const char* what) { return "tensor " + std::to_string(i) + ": " + what; };
+    if (t.dtype != METIS_OUT_F32 && t.dtype != METIS_OUT_BF16) return fail(ctx, METIS_ERR_ARG, at("bad dtype"));
+    if (t.n < 0) return fail(ctx, METIS_ERR_SHAPE, at("negative length"));
+    if (t.id >= (1u << 24)) return fail(ctx, METIS_ERR_ARG, at("id must be below 2^24"));
+    if (t.n == 0) continue;
+    if (!t.p || !t.g || !t.m || !t.v || (q->state_bits == 8 && (!t.m_exponent || !t.v_exponent)))
+      return fail(ctx, METIS_ERR_ARG, at("null array"));
+    const uintptr_t data = reinterpret_cast<uintptr_t>(t.p) | reinterpret_cast<uintptr_t>(t.g);
+    const uintptr_t state = reinterpret_cast<uintptr_t>(t.m) | reinterpret_cast<uintptr_t>(t.v);
+    if ((data & (t.dtype == METIS_OUT_F32 ? 3u : 1u)) || (q->state_bits == 32 && (state & 3u)))
+      return fail(ctx, METIS_ERR_ALIGN, at("an array is not aligned to its element"));
+  }
+  return METIS_OK;
+}
+
+}  // namespace
+}  // namespace metis
+
+extern "C" {
+
+metis_status metis_quantize_int8(metis_ctx* ctx, const void* M, int64_t rows, int64_t cols, int64_t ld, int32_t dtype,
+                                 metis_int8* rowwise, metis_int8* colwise) {
+  const metis::NvtxRange nvtx_range("metis_quantize_int8");
+  return guarded(ctx, [&] {
+    const metis_status s = check_quantize_int8(ctx, M, rows, cols, ld, dtype, rowwise, colwise);
+    if (s != METIS_OK) return s;
+    return check_cuda(ctx, launch_quantize_i8(M, dtype == METIS_OUT_BF16, rows, cols, ld, rowwise, colwise, ctx->status,
+                                              ctx->stream),
+                      "int8 quantize launch");
+  });
+}
+
+metis_status metis_gemm_int8(metis_ctx* ctx, const metis_int8* A, const metis_int8* B, void* C, int64_t ldc,
+                             int32_t c_dtype) {
+  const metis::NvtxRange nvtx_range("metis_gemm_int8");
+  return guarded(ctx, [&] {
+    const metis_status s = check_gemm_int8(ctx, A, B, C, ldc, c_dtype);
+    return s == METIS_OK ? launch_gemm_i8(ctx, A, B, C, ldc, c_dtype) : s;
+  });
+}
+
+metis_status metis_linear_int8(metis_ctx* ctx, const void* X, int64_t ld, int32_t dtype, metis_int8* Xq,
+                               const metis_int8* W, void* C, int64_t ldc, int32_t c_dtype) {
+  const metis::NvtxRange nvtx_range("metis_linear_int8");
+  return guarded(ctx, [&] {
+    if (!Xq) return fail(ctx, METIS_ERR_ARG, "null operand");
+    metis_status s = check_quantize_int8(ctx, X, Xq->outer, Xq->inner, ld, dtype, Xq, nullptr);
+    if (s != METIS_OK || (s = check_gemm_int8(ctx, Xq, W, C, ldc, c_dtype)) != METIS_OK) return s;
+    s = check_cuda(ctx, launch_quantize_i8(X, dtype == METIS_OUT_BF16, Xq->outer, Xq->inner, ld, Xq, nullptr,
+                                           ctx->status, ctx->stream),
+                   "int8 quantize launch");
+    return s == METIS_OK ? launch_gemm_i8(ctx, Xq, W, C, ldc, c_dtype) : s;
+  });
+}
+
+metis_status metis_adamw_step(metis_ctx* ctx, const metis_adamw_tensor* tensors, int64_t count,
+                              const metis_adamw_params* q) {
+  const metis::NvtxRange nvtx_range("metis_adamw_step");
+  return guarded(ctx, [&] {
+    const metis_status s = check_adamw(ctx, tensors, count, q);
+    return s == METIS_OK ? run_adamw(ctx, tensors, count, q) : s;
+  });
+}
+
+}  // extern "C"

@@ -46,7 +46,7 @@ __device__ __forceinline__ Words4 philox10(uint32_t c0, uint32_t c1, uint32_t c2
 
 // Stream layout: key = seed, counter = (q lo, q hi, tag, step),
 // tag = operand_id << 8 | purpose << 4 | sub.
-enum : uint32_t { kPurposeSample = 1, kPurposeOmega = 2, kPurposeSR = 3 };
+enum : uint32_t { kPurposeSample = 1, kPurposeOmega = 2, kPurposeSR = 3, kPurposeState = 4 };
 enum : uint32_t { kSrRowwise = 0, kSrColwise = 1, kSrLeft = 2, kSrRight = 3 };
 
 __host__ __device__ __forceinline__ uint32_t stream_tag(uint32_t operand_id, uint32_t purpose,

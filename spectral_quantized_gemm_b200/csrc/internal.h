@@ -169,6 +169,16 @@ metis_status run_lora_realign(metis_ctx* ctx, float* W, int64_t m, int64_t n, in
                               int k, float beta, const metis_decomp_params* p, uint32_t step, metis_factors* f,
                               void* W_bf16);
 
+// ---- quantize_i8.cu ----
+// Codes and scales of the rows (row, nullable) and of the columns (col, nullable, transposed).
+cudaError_t launch_quantize_i8(const void* M, bool bf16, int64_t rows, int64_t cols, int64_t ld, const metis_int8* row,
+                               const metis_int8* col, uint32_t* status, cudaStream_t st);
+// ---- gemm_i8.cu ----
+metis_status launch_gemm_i8(metis_ctx* ctx, const metis_int8* A, const metis_int8* B, void* C, int64_t ldc,
+                            int32_t c_dtype);
+// ---- adamw.cu ----
+metis_status run_adamw(metis_ctx* ctx, const metis_adamw_tensor* tensors, int64_t count, const metis_adamw_params* q);
+
 // ---- layer.cu ----
 metis_status run_linear(metis_ctx* ctx, const metis_operand* A, const metis_nvfp4* A_res, const metis_operand* B,
                         const metis_nvfp4* B_res, bool a_transposed_factors, bool b_transposed_factors, void* C,

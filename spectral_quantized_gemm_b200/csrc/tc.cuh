@@ -178,6 +178,16 @@ __device__ __forceinline__ void mma_bf16(uint32_t d_tmem, uint64_t adesc, uint64
       : "memory");
 }
 
+// D[tmem] (+)= A[smem] * B[smem]^T, int8 x int8 -> int32.
+__device__ __forceinline__ void mma_i8(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
+                                       uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::i8 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
 // 32 lanes x 32 bits, 32 consecutive columns: thread t of the warp gets lane
 // (quarter base + t), columns [col, col + 32).
 __device__ __forceinline__ void tmem_load_32cols(uint32_t taddr, float (&v)[32]) {
@@ -217,7 +227,12 @@ __device__ __forceinline__ uint32_t cluster_rank() {
   asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
   return r;
 }
-// Barrier over every thread of both CTAs (release / acquire at cluster scope).
+__device__ __forceinline__ uint32_t cluster_size() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
+  return r;
+}
+// Barrier over every thread of all CTAs of the cluster (release / acquire at cluster scope).
 __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
@@ -225,6 +240,12 @@ __device__ __forceinline__ void cluster_sync() {
 __device__ __forceinline__ uint32_t cluster_addr(const void* p, uint32_t rank) {
   uint32_t r;
   asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(smem_addr(p)), "r"(rank));
+  return r;
+}
+// The same for a shared::cta address.
+__device__ __forceinline__ uint32_t cluster_addr_u32(uint32_t saddr, uint32_t rank) {
+  uint32_t r;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(saddr), "r"(rank));
   return r;
 }
 // Arrive (release, cluster scope) on the mbarrier at shared::cluster address `bar`.
@@ -337,6 +358,17 @@ __host__ __device__ __forceinline__ uint32_t idesc_bf16(uint32_t n, uint32_t m =
   d |= 1u << 4;               // D format: fp32
   d |= 1u << 7;               // A format: bf16
   d |= 1u << 10;              // B format: bf16
+  d |= (n >> 3) << 17;
+  d |= (m >> 4) << 24;
+  return d;
+}
+
+// Instruction descriptor: signed int8 x int8 -> int32, both K-major; M = 128 or 256.
+__host__ __device__ __forceinline__ uint32_t idesc_i8(uint32_t n, uint32_t m = 128) {
+  uint32_t d = 0;
+  d |= 2u << 4;               // D format: s32
+  d |= 1u << 7;               // A format: signed 8-bit
+  d |= 1u << 10;              // B format: signed 8-bit
   d |= (n >> 3) << 17;
   d |= (m >> 4) << 24;
   return d;
