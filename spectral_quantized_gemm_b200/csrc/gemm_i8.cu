@@ -12,6 +12,12 @@
 //   warps 2..5  epilogue
 // With few rows of A (tokens) the roles are swapped: B's rows (channels) take the 128
 // lanes of the tile and the tokens its BN columns, so no lane idles.
+//
+// gemm_i8_pair_kernel: large products.  A cluster of two CTAs computes 256 x 256 tiles with
+// cta_group::2 MMAs (each CTA loads 128 rows of A and 128 of B for every 128 K elements),
+// persistent over the tiles, with two accumulators so that the epilogue of a tile runs
+// under the MMAs of the next.
+//
 // Every mbarrier wait is bounded; on expiry the CTA raises METIS_DEV_TIMEOUT, stops
 // issuing work and exits after releasing its tensor memory.
 #include <cuda.h>
@@ -258,6 +264,251 @@ __global__ void __launch_bounds__(kThreads)
   if (splits > 1) tc::cluster_sync();   // no CTA leaves while its sums are still read
 }
 
+// ------------------------------------------------------------------ CTA-pair kernel
+struct PairCfg {
+  static constexpr int STAGE_BYTES = 2 * 128 * 128;
+  static constexpr int STAGES = 6;
+  static constexpr int EPI_WARPS = 8;
+  static constexpr int THREADS = 64 + 32 * EPI_WARPS;
+  static constexpr int BOX_BYTES = 4096;               // 32 rows x 128 bytes of the output, a warp's staging
+  static constexpr size_t SMEM = (size_t)STAGES * STAGE_BYTES + EPI_WARPS * BOX_BYTES + 1024 + 256;
+  static_assert(SMEM <= 232448, "shared memory budget");
+};
+
+struct PairParams {
+  const float* sa;
+  const float* sb;
+  int64_t p, q;
+  void* C;
+  int64_t ldc;
+  int f32;
+  int m_tiles, n_tiles, k_tiles;
+  uint32_t* status;
+};
+
+// Columns of C that the TMA stores write: it clips at the matrix's edge in units of 16 bytes
+// (measured: with 1333 bf16 columns it wrote 1336), so the odd last ones leave by plain stores.
+inline __host__ __device__ int64_t whole_columns(int64_t q, int f32) { return f32 ? q & ~int64_t(3) : q & ~int64_t(7); }
+
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairCfg::THREADS, 1)
+    gemm_i8_pair_kernel(const __grid_constant__ CUtensorMap mapA, const __grid_constant__ CUtensorMap mapB,
+                        const __grid_constant__ CUtensorMap mapC, const PairParams p) {
+  using C = PairCfg;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* epi = smem + C::STAGES * C::STAGE_BYTES;
+  uint64_t* bars = reinterpret_cast<uint64_t*>(epi + C::EPI_WARPS * C::BOX_BYTES);
+  uint64_t* full = bars;                       // (even CTA) the pair's stage landed
+  uint64_t* empty = bars + C::STAGES;          // the pair's MMAs are done with the stage
+  uint64_t* acc_full = bars + 2 * C::STAGES;   // [2] this CTA's accumulator is complete
+  uint64_t* acc_empty = acc_full + 2;          // [2] (even CTA) both CTAs have read theirs
+  uint64_t* drain = acc_full + 4;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(acc_full + 5);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = tc::cluster_rank();
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < C::STAGES; ++s) {
+      tc::mbar_init(&full[s], 1);
+      tc::mbar_init(&empty[s], 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      tc::mbar_init(&acc_full[b], 1);
+      tc::mbar_init(&acc_empty[b], 2 * C::EPI_WARPS);
+    }
+    tc::mbar_init(drain, 1);
+    *abort_flag = 0;
+    tc::fence_barrier_init();
+    tc::prefetch_tensormap(&mapA);
+    tc::prefetch_tensormap(&mapB);
+    tc::prefetch_tensormap(&mapC);
+  }
+  if (warp == 1) {
+    tc::tmem_alloc_pair(tmem_slot, 512);
+    tc::tmem_relinquish_pair();
+  }
+  tc::tc_fence_before();
+  __syncthreads();
+  tc::cluster_sync();   // both CTAs' barriers exist before any cross-CTA arrival
+  tc::tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+
+  const int pair = blockIdx.x >> 1, npairs = gridDim.x >> 1;
+  const int num_tiles = p.m_tiles * p.n_tiles;
+
+  if (warp == 0) {
+    // ------------------------------------------------------------ producer (both CTAs)
+    if (lane == 0) {
+      const uint32_t full0 = tc::cluster_addr(&full[0], 0);
+      int stage = 0;
+      int64_t issued = 0;
+      uint32_t phase = 0;
+      for (int tile = pair; tile < num_tiles && !*abort_flag; tile += npairs) {
+        const int arow = (tile % p.m_tiles) * 256 + (int)rank * 128;
+        const int brow = (tile / p.m_tiles) * 256 + (int)rank * 128;
+        for (int kk = 0; kk < p.k_tiles; ++kk) {
+          if (!tc::mbar_wait(&empty[stage], phase ^ 1u, abort_flag)) {
+            *abort_flag = 1;
+            raise_status(p.status, METIS_DEV_TIMEOUT);
+            break;
+          }
+          uint8_t* sa = smem + stage * C::STAGE_BYTES;
+          const uint32_t fb = full0 + 8u * (uint32_t)stage;
+          if (rank == 0) tc::mbar_expect_tx(&full[stage], 2 * C::STAGE_BYTES);
+          tc::tma_load_2d_pair(sa, &mapA, fb, kk * 128, arow);
+          tc::tma_load_2d_pair(sa + 128 * 128, &mapB, fb, kk * 128, brow);
+          if (++stage == C::STAGES) {
+            stage = 0;
+            phase ^= 1u;
+          }
+          ++issued;
+        }
+      }
+      // after a timeout too, no load of the pair is in flight past the last cluster barrier
+      if (rank == 0)
+        for (int k = (int)min(issued, (int64_t)C::STAGES); k > 0; --k) {
+          if (--stage < 0) {
+            stage = C::STAGES - 1;
+            phase ^= 1u;
+          }
+          tc::mbar_wait(&full[stage], phase, nullptr, tc::kWaitLimitCycles / 8);
+        }
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    // ------------------------------------------------------------ MMA issuer (even CTA)
+    if (lane == 0 && rank == 0) {
+      int stage = 0, it = 0;
+      uint32_t phase = 0;
+      const uint32_t id = tc::idesc_i8(256, 256);
+      for (int tile = pair; tile < num_tiles && !*abort_flag; tile += npairs, ++it) {
+        const int buf = it & 1;
+        if (!tc::mbar_wait(&acc_empty[buf], ((uint32_t)(it >> 1) & 1u) ^ 1u, abort_flag)) {
+          *abort_flag = 1;
+          raise_status(p.status, METIS_DEV_TIMEOUT);
+          break;
+        }
+        tc::tc_fence_after();
+        const uint32_t acc = tmem + (uint32_t)buf * 256u;
+        for (int kk = 0; kk < p.k_tiles; ++kk) {
+          if (!tc::mbar_wait(&full[stage], phase, abort_flag)) {
+            *abort_flag = 1;
+            raise_status(p.status, METIS_DEV_TIMEOUT);
+            break;
+          }
+          tc::tc_fence_after();
+          const uint32_t sa = tc::smem_addr(smem + stage * C::STAGE_BYTES);
+          const uint64_t ad = tc::sdesc_sw128(sa), bd = tc::sdesc_sw128(sa + 128 * 128);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) tc::mma_i8_pair(acc, ad + 2 * j, bd + 2 * j, id, (kk || j) ? 1u : 0u);
+          tc::tc_commit_pair(&empty[stage], 0x3);
+          if (++stage == C::STAGES) {
+            stage = 0;
+            phase ^= 1u;
+          }
+        }
+        if (*abort_flag) break;
+        tc::tc_commit_pair(&acc_full[buf], 0x3);
+      }
+      // let every issued tensor-core operation finish before the memory is released
+      tc::tc_commit_pair(drain, 0x1);
+      tc::mbar_wait(drain, 0, nullptr);
+    }
+    __syncwarp();
+  } else {
+    // ------------------------------------------------------------ epilogue (both CTAs)
+    // A warp takes 32 rows x 128 columns in pieces of one output box (128 bytes a row:
+    // 64 bf16 or 32 fp32 columns): sums -> registers -> scaled into the swizzled box -> TMA
+    // store, clipped at the matrix's edges.
+    const int quarter = warp & 3, half = (warp - 2) >> 2;
+    const uint32_t empty_bar = tc::cluster_addr(&acc_empty[0], 0);
+    uint8_t* box = epi + (warp - 2) * C::BOX_BYTES;
+    const int swz = lane & 7;   // 16-byte chunk j of a box row r sits at position j ^ (r mod 8)
+    int it = 0;
+    for (int tile = pair; tile < num_tiles; tile += npairs, ++it) {
+      const int buf = it & 1;
+      const bool ok = __all_sync(0xffffffffu, tc::mbar_wait(&acc_full[buf], (uint32_t)(it >> 1) & 1u, abort_flag));
+      if (!ok) {
+        if (lane == 0) {
+          *abort_flag = 1;
+          raise_status(p.status, METIS_DEV_TIMEOUT);
+        }
+        break;
+      }
+      tc::tc_fence_after();
+      const int y = (tile % p.m_tiles) * 256 + (int)rank * 128 + quarter * 32;
+      const int x0 = (tile / p.m_tiles) * 256 + half * 128;
+      const float sa = y + lane < p.p ? p.sa[y + lane] : 0.0f;
+      const uint32_t acc = tmem + (uint32_t)buf * 256u + ((uint32_t)(quarter * 32) << 16) + (uint32_t)(half * 128);
+      const int last = (int)p.q - 1, whole = (int)whole_columns(p.q, p.f32);
+#pragma unroll
+      for (int c = 0; c < 128; c += 32) {
+        float v[32];
+        tc::tmem_load_32cols(acc + (uint32_t)c, v);
+        tc::tmem_load_wait();
+        if (c == 96) {
+          tc::tc_fence_before();
+          __syncwarp();
+          if (lane == 0) tc::mbar_arrive_cluster(empty_bar + 8u * (uint32_t)buf);
+        }
+#pragma unroll
+        for (int i = 0; i < 32; ++i) v[i] = (float)__float_as_int(v[i]) * sa * p.sb[min(x0 + c + i, last)];
+        if (whole <= last && x0 + c <= last && x0 + c + 32 > whole && y + lane < p.p) {
+          const int64_t at = (int64_t)(y + lane) * p.ldc + x0 + c;
+#pragma unroll
+          for (int i = 0; i < 32; ++i)
+            if (x0 + c + i >= whole && x0 + c + i <= last) {
+              if (p.f32) static_cast<float*>(p.C)[at + i] = v[i];
+              else static_cast<__nv_bfloat16*>(p.C)[at + i] = __float2bfloat16_rn(v[i]);
+            }
+        }
+        if (p.f32 || c % 64 == 0) {
+          if (lane == 0) tc::bulk_wait_read_all();   // the last store has left the box
+          __syncwarp();
+        }
+        if (p.f32) {
+#pragma unroll
+          for (int j = 0; j < 8; ++j)
+            *reinterpret_cast<float4*>(box + lane * 128 + ((j ^ swz) << 4)) =
+                make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
+        } else {
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            uint32_t w[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const __nv_bfloat162 pr = __floats2bfloat162_rn(v[8 * j + 2 * i], v[8 * j + 2 * i + 1]);
+              w[i] = *reinterpret_cast<const uint32_t*>(&pr);
+            }
+            *reinterpret_cast<uint4*>(box + lane * 128 + (((j + (c % 64) / 8) ^ swz) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
+          }
+        }
+        if (p.f32 || c % 64 == 32) {
+          tc::fence_proxy_async();
+          __syncwarp();
+          const int x = x0 + (p.f32 ? c : c - 32);
+          if (lane == 0 && x < whole && y < p.p) {
+            tc::tma_store_2d(&mapC, box, x, y);
+            tc::bulk_commit_group();
+          }
+        }
+      }
+    }
+    if (lane == 0) tc::bulk_wait_all();   // stores complete before the boxes go away
+    __syncwarp();
+  }
+
+  tc::tc_fence_before();
+  __syncthreads();
+  tc::cluster_sync();   // no cross-CTA access is outstanding past this point
+  if (warp == 1) {
+    tc::tc_fence_after();
+    tc::tmem_dealloc_pair(tmem, 512);
+  }
+}
+
 bool make_map_i8(CUtensorMap* map, const metis_int8* t, uint32_t box_rows) {
   const cuuint64_t dims[2] = {(cuuint64_t)t->inner, (cuuint64_t)t->outer};
   const cuuint64_t strides[1] = {(cuuint64_t)t->ld};
@@ -301,6 +552,34 @@ metis_status launch_tile(metis_ctx* ctx, const metis_int8* A, const metis_int8* 
   return METIS_OK;
 }
 
+bool make_map_out(CUtensorMap* map, const Params& prm) {
+  const cuuint64_t dims[2] = {(cuuint64_t)whole_columns(prm.q, prm.f32), (cuuint64_t)prm.p};
+  const cuuint64_t strides[1] = {(cuuint64_t)prm.ldc * (prm.f32 ? 4 : 2)};
+  const cuuint32_t box[2] = {prm.f32 ? 32u : 64u, 32};
+  const cuuint32_t estr[2] = {1, 1};
+  EncodeTiledFn enc = encode_tiled();
+  if (!enc) return false;
+  return enc(map, prm.f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, prm.C, dims, strides,
+             box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+metis_status launch_pair(metis_ctx* ctx, const metis_int8* A, const metis_int8* B, const Params& prm) {
+  using C = PairCfg;
+  CUtensorMap ma, mb, mc;
+  if (!make_map_i8(&ma, A, 128) || !make_map_i8(&mb, B, 128) || !make_map_out(&mc, prm))
+    return fail(ctx, METIS_ERR_CUDA, "cuTensorMapEncodeTiled failed for the int8 product");
+  const int64_t m_tiles = (prm.p + 255) / 256, n_tiles = (prm.q + 255) / 256;
+  if (m_tiles * n_tiles > INT32_MAX / 2) return fail(ctx, METIS_ERR_SHAPE, "too many output tiles");
+  const PairParams pp{prm.sa, prm.sb, prm.p, prm.q, prm.C, prm.ldc, prm.f32, (int)m_tiles, (int)n_tiles, prm.k_tiles, prm.status};
+  const cudaError_t e = cudaFuncSetAttribute(gemm_i8_pair_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::SMEM);
+  if (e != cudaSuccess) return check_cuda(ctx, e, "cudaFuncSetAttribute(int8 gemm pair)");
+  const int grid = 2 * (int)std::min<int64_t>(m_tiles * n_tiles, ctx->sm_count / 2);
+  gemm_i8_pair_kernel<<<grid, C::THREADS, C::SMEM, ctx->stream>>>(ma, mb, mc, pp);
+  count_launch();
+  return check_cuda(ctx, cudaGetLastError(), "int8 gemm pair launch");
+}
+
 }  // namespace
 
 metis_status launch_gemm_i8(metis_ctx* ctx, const metis_int8* A, const metis_int8* B, void* C, int64_t ldc,
@@ -315,6 +594,7 @@ metis_status launch_gemm_i8(metis_ctx* ctx, const metis_int8* A, const metis_int
   prm.f32 = c_dtype == METIS_OUT_F32;
   prm.k_tiles = (int)((A->inner + 127) / 128);
   prm.status = ctx->status;
+  if (prm.p >= 512 && prm.q >= 512) return launch_pair(ctx, A, B, prm);
   return launch_tile<128, false>(ctx, A, B, prm, 1);
 }
 
