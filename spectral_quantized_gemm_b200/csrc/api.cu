@@ -698,7 +698,7 @@ metis_status metis_gemm_int8(metis_ctx* ctx, const metis_int8* A, const metis_in
   const metis::NvtxRange nvtx_range("metis_gemm_int8");
   return guarded(ctx, [&] {
     const metis_status s = check_gemm_int8(ctx, A, B, C, ldc, c_dtype);
-    return s == METIS_OK ? launch_gemm_i8(ctx, A, B, C, ldc, c_dtype) : s;
+    return s == METIS_OK ? launch_gemm_i8(ctx, A, B, C, ldc, c_dtype, false) : s;
   });
 }
 
@@ -712,7 +712,7 @@ metis_status metis_linear_int8(metis_ctx* ctx, const void* X, int64_t ld, int32_
     s = check_cuda(ctx, launch_quantize_i8(X, dtype == METIS_OUT_BF16, Xq->outer, Xq->inner, ld, Xq, nullptr,
                                            ctx->status, ctx->stream),
                    "int8 quantize launch");
-    return s == METIS_OK ? launch_gemm_i8(ctx, Xq, W, C, ldc, c_dtype) : s;
+    return s == METIS_OK ? launch_gemm_i8(ctx, Xq, W, C, ldc, c_dtype, true) : s;
   });
 }
 

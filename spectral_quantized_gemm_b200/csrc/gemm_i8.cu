@@ -4,14 +4,16 @@
 // sum is exact (K <= 131071 keeps it below 2^31); it is rounded to fp32 once, then
 // multiplied by sA[i] and by sB[j], then rounded to the output type.
 //
-// gemm_i8_kernel: a cluster of S CTAs computes one 128 x BN tile, each CTA a share of K;
-// the int32 sums are joined through distributed shared memory (the order of integer
-// additions does not matter) and every CTA writes its part of the tile.
+// gemm_i8_kernel: a cluster of S CTAs computes one tile of 128 rows of B (channels, on the
+// lanes of tensor memory) by BN rows of A (tokens), each CTA a share of K; the int32 sums are
+// joined through distributed shared memory (the order of integer additions does not matter)
+// and every CTA writes its part of the tile.
 //   warp 0      TMA producer, 128-byte swizzled tiles of 128 K elements; zeros past the edges
 //   warp 1      tensor-memory owner and MMA issuer (one thread)
 //   warps 2..5  epilogue
-// With few rows of A (tokens) the roles are swapped: B's rows (channels) take the 128
-// lanes of the tile and the tokens its BN columns, so no lane idles.
+// Channels on the lanes suit few tokens (no lane idles) and let the staged sums be written
+// and read without bank conflicts; at 512 x 768 x 2304 the other way round took 7.5 us, this
+// one 7.1.
 //
 // gemm_i8_pair_kernel: large products.  A cluster of two CTAs computes 256 x 256 tiles with
 // cta_group::2 MMAs (each CTA loads 128 rows of A and 128 of B for every 128 K elements),
@@ -34,7 +36,6 @@ namespace metis {
 namespace {
 
 constexpr int kThreads = 192;
-constexpr int kEpiThreads = 128;
 
 struct Params {
   const float* sa;
@@ -43,24 +44,28 @@ struct Params {
   int64_t ldc;
   int64_t p, q;          // rows and columns of C
   int f32;
-  int lane_tiles;        // 128-row blocks of the operand on the lanes
+  int lane_tiles;        // 128-row blocks of B
   int k_tiles;           // 128-element blocks of K
+  int early;             // B may be read before the preceding kernel has ended
   uint32_t* status;
 };
 
 template <int BN>
 struct Cfg {
-  static constexpr int A_BYTES = 128 * 128;
-  static constexpr int B_BYTES = BN * 128;
+  static constexpr int A_BYTES = BN * 128;             // tokens
+  static constexpr int B_BYTES = 128 * 128;            // channels
   static constexpr int STAGE_BYTES = A_BYTES + B_BYTES;
-  static constexpr int STAGES = BN <= 64 ? 4 : 3;      // two CTAs fit an SM
   static constexpr int TMEM_COLS = BN < 32 ? 32 : BN;
-  // staged sums: rows of the output, 4 words of padding so that 16-byte accesses of
-  // consecutive rows fall on different banks
-  static constexpr int STAGED = (BN + 4) * 128 > (128 + 4) * BN ? (BN + 4) * 128 * 4 : (128 + 4) * BN * 4;
+  // Three CTAs fit an SM (BN 16 and 32), or two (64).  Rings of up to 12 stages, one CTA an SM,
+  // were no faster (40 x 4096 x 4096: 11.9 us, 4 stages 10.6) and leave clusters fewer places.
+  static constexpr int STAGES = BN == 32 ? 3 : 4;
+  static constexpr int PER_SM = BN == 64 ? 2 : 3;
   static constexpr int RING = STAGES * STAGE_BYTES;
-  static constexpr size_t SMEM = (size_t)(RING > STAGED ? RING : STAGED) + 1024 + 256;
-  static_assert(SMEM <= 116000, "two CTAs an SM");
+  static constexpr int PITCH = 128 + 4;                // words of a staged row of sums
+  static constexpr int SCALES = (128 + BN) * 4;
+  static constexpr size_t SMEM = (size_t)RING + SCALES + 1024 + 256;
+  static_assert(BN * PITCH * 4 <= RING, "the sums take the ring's place");
+  static_assert((SMEM + 1024) * PER_SM <= 233472, "CTAs an SM");
 };
 
 __device__ __forceinline__ int4 load_cluster_int4(uint32_t addr) {
@@ -69,14 +74,15 @@ __device__ __forceinline__ int4 load_cluster_int4(uint32_t addr) {
   return v;
 }
 
-template <int BN, bool SWAP>
+template <int BN>
 __global__ void __launch_bounds__(kThreads)
-    gemm_i8_kernel(const __grid_constant__ CUtensorMap map_lane, const __grid_constant__ CUtensorMap map_col,
-                   const Params p) {
+    gemm_i8_kernel(const __grid_constant__ CUtensorMap mapA, const __grid_constant__ CUtensorMap mapB, const Params p) {
   using C = Cfg<BN>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + (C::RING > C::STAGED ? C::RING : C::STAGED));
+  float* sb = reinterpret_cast<float*>(smem + C::RING);   // scales of the tile's channels and tokens
+  float* sa = sb + 128;
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::RING + C::SCALES);
   uint64_t* full = bars;
   uint64_t* empty = bars + C::STAGES;
   uint64_t* done = bars + 2 * C::STAGES;
@@ -98,8 +104,8 @@ __global__ void __launch_bounds__(kThreads)
     tc::mbar_init(done, 1);
     *abort_flag = 0;
     tc::fence_barrier_init();
-    tc::prefetch_tensormap(&map_lane);
-    tc::prefetch_tensormap(&map_col);
+    tc::prefetch_tensormap(&mapA);
+    tc::prefetch_tensormap(&mapB);
   }
   if (warp == 1) {
     tc::tmem_alloc(tmem_slot, C::TMEM_COLS);
@@ -112,18 +118,30 @@ __global__ void __launch_bounds__(kThreads)
 
   if (warp == 0) {
     if (lane == 0) {
-      int stage = 0, issued = 0;
-      uint32_t phase = 0;
-      for (int kk = s0; kk < s1; ++kk) {
+      // the first round of the ring; B's tiles may go out under the tail of the preceding kernel
+      const int first = min(C::STAGES, s1 - s0);
+      for (int s = 0; s < first; ++s) {
+        tc::mbar_expect_tx(&full[s], C::STAGE_BYTES);
+        tc::tma_load_2d(smem + s * C::STAGE_BYTES + C::A_BYTES, &mapB, &full[s], (s0 + s) * 128, lb * 128);
+        if (!p.early) tc::tma_load_2d(smem + s * C::STAGE_BYTES, &mapA, &full[s], (s0 + s) * 128, cb * BN);
+      }
+      if (p.early) {
+        tc::grid_dependency_wait();
+        for (int s = 0; s < first; ++s)
+          tc::tma_load_2d(smem + s * C::STAGE_BYTES, &mapA, &full[s], (s0 + s) * 128, cb * BN);
+      }
+      int stage = first == C::STAGES ? 0 : first, issued = first;
+      uint32_t phase = first == C::STAGES ? 1u : 0u;
+      for (int kk = s0 + first; kk < s1; ++kk) {
         if (!tc::mbar_wait(&empty[stage], phase ^ 1u, abort_flag)) {
           *abort_flag = 1;
           raise_status(p.status, METIS_DEV_TIMEOUT);
           break;
         }
-        uint8_t* sa = smem + stage * C::STAGE_BYTES;
+        uint8_t* at = smem + stage * C::STAGE_BYTES;
         tc::mbar_expect_tx(&full[stage], C::STAGE_BYTES);
-        tc::tma_load_2d(sa, &map_lane, &full[stage], kk * 128, lb * 128);
-        tc::tma_load_2d(sa + C::A_BYTES, &map_col, &full[stage], kk * 128, cb * BN);
+        tc::tma_load_2d(at + C::A_BYTES, &mapB, &full[stage], kk * 128, lb * 128);
+        tc::tma_load_2d(at, &mapA, &full[stage], kk * 128, cb * BN);
         if (++stage == C::STAGES) {
           stage = 0;
           phase ^= 1u;
@@ -152,10 +170,10 @@ __global__ void __launch_bounds__(kThreads)
           break;
         }
         tc::tc_fence_after();
-        const uint32_t sa = tc::smem_addr(smem + stage * C::STAGE_BYTES);
-        const uint64_t ad = tc::sdesc_sw128(sa), bd = tc::sdesc_sw128(sa + C::A_BYTES);
+        const uint32_t at = tc::smem_addr(smem + stage * C::STAGE_BYTES);
+        const uint64_t lanes = tc::sdesc_sw128(at + C::A_BYTES), cols = tc::sdesc_sw128(at);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) tc::mma_i8(tmem, ad + 2 * j, bd + 2 * j, id, (kk != s0 || j) ? 1u : 0u);
+        for (int j = 0; j < 4; ++j) tc::mma_i8(tmem, lanes + 2 * j, cols + 2 * j, id, (kk != s0 || j) ? 1u : 0u);
         tc::tc_commit(&empty[stage]);
         if (++stage == C::STAGES) {
           stage = 0;
@@ -170,6 +188,13 @@ __global__ void __launch_bounds__(kThreads)
       }
     }
     __syncwarp();
+  } else {
+    // the tile's scales, fetched while the sums are made
+    const int t = (int)threadIdx.x - 64;
+    const int64_t j = (int64_t)lb * 128 + t;
+    sb[t] = j < p.q ? p.sb[j] : 0.0f;
+    if (p.early) tc::grid_dependency_wait();
+    if (t < BN) sa[t] = (int64_t)cb * BN + t < p.p ? p.sa[(int64_t)cb * BN + t] : 0.0f;
   }
   // All loads have landed and all MMAs are done once every thread is here: the ring's
   // memory becomes the staging buffer.
@@ -187,15 +212,8 @@ __global__ void __launch_bounds__(kThreads)
       const uint32_t addr = tmem + ((uint32_t)(quarter * 32) << 16) + (uint32_t)c;
       if constexpr (W == 16) tc::tmem_load_16cols(addr, f); else tc::tmem_load_32cols(addr, f);
       tc::tmem_load_wait();
-      if constexpr (SWAP) {
 #pragma unroll
-        for (int i = 0; i < W; ++i) staged[(c + i) * (128 + 4) + row] = __float_as_int(f[i]);
-      } else {
-#pragma unroll
-        for (int i = 0; i < W; i += 4)
-          *reinterpret_cast<int4*>(staged + row * (BN + 4) + c + i) =
-              make_int4(__float_as_int(f[i]), __float_as_int(f[i + 1]), __float_as_int(f[i + 2]), __float_as_int(f[i + 3]));
-      }
+      for (int i = 0; i < W; ++i) staged[(c + i) * C::PITCH + row] = __float_as_int(f[i]);
     }
   }
   tc::tc_fence_before();
@@ -206,15 +224,15 @@ __global__ void __launch_bounds__(kThreads)
     tc::tmem_dealloc(tmem, C::TMEM_COLS);
   }
   // This CTA's part of the tile: runs of 8 columns of C, a 16-byte store of bf16 or two of fp32.
-  {
-    constexpr int ROWS = SWAP ? BN : 128, COLS = SWAP ? 128 : BN, RUNS = COLS / 8;
-    const int64_t r0 = SWAP ? (int64_t)cb * BN : (int64_t)lb * 128, c0 = SWAP ? (int64_t)lb * 128 : (int64_t)cb * BN;
+  if (warp >= 2) {
+    constexpr int RUNS = 128 / 8;
+    const int64_t r0 = (int64_t)cb * BN, c0 = (int64_t)lb * 128;
     const uint32_t mine = tc::smem_addr(staged);
-    const int u1 = ROWS * RUNS * (split + 1) / splits;
-    for (int u = ROWS * RUNS * split / splits + (int)threadIdx.x; u < u1; u += kThreads) {
+    const int u1 = BN * RUNS * (split + 1) / splits;
+    for (int u = BN * RUNS * split / splits + (int)threadIdx.x - 64; u < u1; u += kThreads - 64) {
       const int64_t i = r0 + u / RUNS, j = c0 + (u % RUNS) * 8;
       if (i >= p.p || j >= p.q) continue;
-      const uint32_t off = (uint32_t)((u / RUNS) * (COLS + 4) + (u % RUNS) * 8) * 4u;
+      const uint32_t off = (uint32_t)((u / RUNS) * C::PITCH + (u % RUNS) * 8) * 4u;
       int acc[8] = {};
       if (splits == 1) {
         const int4 a = *reinterpret_cast<const int4*>(smem + off), b = *reinterpret_cast<const int4*>(smem + off + 16);
@@ -228,11 +246,11 @@ __global__ void __launch_bounds__(kThreads)
           acc[4] += b.x; acc[5] += b.y; acc[6] += b.z; acc[7] += b.w;
         }
       }
-      const float sa = p.sa[i];
+      const float si = sa[u / RUNS];
       const bool whole = j + 8 <= p.q;
       float o[8];
 #pragma unroll
-      for (int e = 0; e < 8; ++e) o[e] = (float)acc[e] * sa * (j + e < p.q ? p.sb[j + e] : 0.0f);
+      for (int e = 0; e < 8; ++e) o[e] = (float)acc[e] * si * sb[(u % RUNS) * 8 + e];
       if (p.f32) {
         float* dst = static_cast<float*>(p.C) + i * p.ldc + j;
         if (whole) {
@@ -521,32 +539,35 @@ bool make_map_i8(CUtensorMap* map, const metis_int8* t, uint32_t box_rows) {
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int BN, bool SWAP>
-metis_status launch_tile(metis_ctx* ctx, const metis_int8* A, const metis_int8* B, Params prm, int splits) {
+template <int BN>
+metis_status launch_tile(metis_ctx* ctx, const metis_int8* A, const metis_int8* B, Params prm, int splits, bool chained) {
   using C = Cfg<BN>;
-  const metis_int8 *on_lanes = SWAP ? B : A, *on_cols = SWAP ? A : B;
-  CUtensorMap ml, mc;
-  if (!make_map_i8(&ml, on_lanes, 128) || !make_map_i8(&mc, on_cols, BN))
+  CUtensorMap ma, mb;
+  if (!make_map_i8(&ma, A, BN) || !make_map_i8(&mb, B, 128))
     return fail(ctx, METIS_ERR_CUDA, "cuTensorMapEncodeTiled failed for the int8 operands");
-  const int64_t lane_tiles = (on_lanes->outer + 127) / 128, col_tiles = (on_cols->outer + BN - 1) / BN;
-  if (lane_tiles * col_tiles * splits > INT32_MAX) return fail(ctx, METIS_ERR_SHAPE, "too many output tiles");
+  const int64_t lane_tiles = (prm.q + 127) / 128, col_tiles = (prm.p + BN - 1) / BN;
+  const int64_t ctas = lane_tiles * col_tiles * splits;
+  if (ctas > INT32_MAX) return fail(ctx, METIS_ERR_SHAPE, "too many output tiles");
   prm.lane_tiles = (int)lane_tiles;
-  auto kern = gemm_i8_kernel<BN, SWAP>;
+  auto kern = gemm_i8_kernel<BN>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::SMEM);
   if (e != cudaSuccess) return check_cuda(ctx, e, "cudaFuncSetAttribute(int8 gemm)");
+  prm.early = chained;
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3((unsigned)(lane_tiles * col_tiles * splits));
+  cfg.gridDim = dim3((unsigned)ctas);
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = C::SMEM;
   cfg.stream = ctx->stream;
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = (unsigned)splits;
   attr[0].val.clusterDim.y = 1;
   attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  e = cudaLaunchKernelEx(&cfg, kern, ml, mc, prm);
+  cfg.numAttrs = chained ? 2 : 1;
+  e = cudaLaunchKernelEx(&cfg, kern, ma, mb, prm);
   if (e != cudaSuccess) return check_cuda(ctx, e, "int8 gemm launch");
   count_launch();
   return METIS_OK;
@@ -583,7 +604,7 @@ metis_status launch_pair(metis_ctx* ctx, const metis_int8* A, const metis_int8* 
 }  // namespace
 
 metis_status launch_gemm_i8(metis_ctx* ctx, const metis_int8* A, const metis_int8* B, void* C, int64_t ldc,
-                            int32_t c_dtype) {
+                            int32_t c_dtype, bool chained) {
   Params prm{};
   prm.sa = A->scales;
   prm.sb = B->scales;
@@ -594,8 +615,23 @@ metis_status launch_gemm_i8(metis_ctx* ctx, const metis_int8* A, const metis_int
   prm.f32 = c_dtype == METIS_OUT_F32;
   prm.k_tiles = (int)((A->inner + 127) / 128);
   prm.status = ctx->status;
-  if (prm.p >= 512 && prm.q >= 512) return launch_pair(ctx, A, B, prm);
-  return launch_tile<128, false>(ctx, A, B, prm, 1);
+  const int bn = prm.p <= 16 ? 16 : prm.p <= 32 ? 32 : 64;
+  const int64_t tiles = ((prm.q + 127) / 128) * ((prm.p + bn - 1) / bn);
+  // Tile kernel or CTA pairs.  While the tiles of the former fit the SMs at once (two each) it is
+  // ahead: 512 x 4096 x 4096 16.7 us against 19.0, 1024 x 1024 x 1024 7.1 against 9.9; with a
+  // second wave it is behind: 2048 x 512 x 2048 13.3 against 10.3.  Up to 128 rows of A leave half
+  // of a pair's tile empty.
+  if (prm.p > 128 && tiles > 2 * ctx->sm_count) return launch_pair(ctx, A, B, prm);
+  // Shares of K.  Up to 16 tokens a join costs little, and more CTAs stream the weight faster
+  // (1 x 4096 x 4096: 12.8 us in one share, 8.2 in eight; 1 x 4096 x 14336: 15.2, 13.8 in three,
+  // 17.3 in four, which no longer fit the SMs three to each).  With 32 or 64 the join moves more:
+  // one CTA an SM and eight blocks of K each (40 x 4096 x 4096: 14.1, 10.3 in four, 12.6 in eight;
+  // 512 x 2304 x 768: 9.6, 9.1 in two, 10.0 in three).
+  const int64_t room = (bn == 16 ? ctx->sm_count * 27 / 10 : ctx->sm_count) / tiles;
+  const int splits = (int)std::max<int64_t>(1, std::min<int64_t>({8, room, prm.k_tiles / (bn == 16 ? 4 : 8)}));
+  if (bn == 16) return launch_tile<16>(ctx, A, B, prm, splits, chained);
+  if (bn == 32) return launch_tile<32>(ctx, A, B, prm, splits, chained);
+  return launch_tile<64>(ctx, A, B, prm, splits, chained);
 }
 
 }  // namespace metis

@@ -174,8 +174,10 @@ metis_status run_lora_realign(metis_ctx* ctx, float* W, int64_t m, int64_t n, in
 cudaError_t launch_quantize_i8(const void* M, bool bf16, int64_t rows, int64_t cols, int64_t ld, const metis_int8* row,
                                const metis_int8* col, uint32_t* status, cudaStream_t st);
 // ---- gemm_i8.cu ----
+// chained: the launch before it on the stream is the quantizer that wrote A, itself an ordinary
+// launch, so that B is complete when this kernel starts early.
 metis_status launch_gemm_i8(metis_ctx* ctx, const metis_int8* A, const metis_int8* B, void* C, int64_t ldc,
-                            int32_t c_dtype);
+                            int32_t c_dtype, bool chained);
 // ---- adamw.cu ----
 metis_status run_adamw(metis_ctx* ctx, const metis_adamw_tensor* tensors, int64_t count, const metis_adamw_params* q);
 

@@ -13,6 +13,7 @@
 
 #include "device_common.cuh"
 #include "internal.h"
+#include "tc.cuh"
 
 namespace metis {
 namespace {
@@ -111,6 +112,7 @@ __global__ void __launch_bounds__(256) quantize_i8_rows_kernel(const T* __restri
                                                                int64_t ld, int8_t* __restrict__ codes, int64_t ldq,
                                                                float* __restrict__ scales, uint32_t* status) {
   __shared__ uint32_t part[8];
+  tc::grid_launch_dependents();   // a product that follows may start loading its other operand
   const int64_t r = blockIdx.x;
   const T* row = M + r * ld;
   const bool vec = (reinterpret_cast<uintptr_t>(row) & 15u) == 0;
