@@ -46,6 +46,7 @@ struct Params {
   int f32;
   int lane_tiles;        // 128-row blocks of B
   int k_tiles;           // 128-element blocks of K
+  int stages;            // of the ring
   int early;             // B may be read before the preceding kernel has ended
   uint32_t* status;
 };
@@ -56,16 +57,19 @@ struct Cfg {
   static constexpr int B_BYTES = 128 * 128;            // channels
   static constexpr int STAGE_BYTES = A_BYTES + B_BYTES;
   static constexpr int TMEM_COLS = BN < 32 ? 32 : BN;
-  // Three CTAs fit an SM (BN 16 and 32), or two (64).  Rings of up to 12 stages, one CTA an SM,
-  // were no faster (40 x 4096 x 4096: 11.9 us, 4 stages 10.6) and leave clusters fewer places.
+  // Three CTAs fit an SM (BN 16 and 32), or two (64); a CTA that has its SM to itself takes a
+  // deeper ring.
   static constexpr int STAGES = BN == 32 ? 3 : 4;
+  static constexpr int DEEP = STAGES;
   static constexpr int PER_SM = BN == 64 ? 2 : 3;
-  static constexpr int RING = STAGES * STAGE_BYTES;
   static constexpr int PITCH = 128 + 4;                // words of a staged row of sums
-  static constexpr int SCALES = (128 + BN) * 4;
-  static constexpr size_t SMEM = (size_t)RING + SCALES + 1024 + 256;
-  static_assert(BN * PITCH * 4 <= RING, "the sums take the ring's place");
-  static_assert((SMEM + 1024) * PER_SM <= 233472, "CTAs an SM");
+  static constexpr int STAGED = BN * PITCH * 4;        // they take the ring's place
+  static constexpr int __host__ __device__ ring(int stages) {
+    return stages * STAGE_BYTES > STAGED ? stages * STAGE_BYTES : STAGED;
+  }
+  static constexpr size_t smem(int stages) { return (size_t)ring(stages) + (128 + BN) * 4 + 1024 + 256; }
+  static_assert(STAGED % 16 == 0 && (smem(STAGES) + 1024) * PER_SM <= 233472, "CTAs an SM");
+  static_assert(smem(DEEP) <= 232448, "shared memory budget");
 };
 
 __device__ __forceinline__ int4 load_cluster_int4(uint32_t addr) {
@@ -74,18 +78,18 @@ __device__ __forceinline__ int4 load_cluster_int4(uint32_t addr) {
   return v;
 }
 
-template <int BN>
+template <int BN, typename OUT>
 __global__ void __launch_bounds__(kThreads)
     gemm_i8_kernel(const __grid_constant__ CUtensorMap mapA, const __grid_constant__ CUtensorMap mapB, const Params p) {
   using C = Cfg<BN>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  float* sb = reinterpret_cast<float*>(smem + C::RING);   // scales of the tile's channels and tokens
+  float* sb = reinterpret_cast<float*>(smem + C::ring(p.stages));   // scales of the tile's channels and tokens
   float* sa = sb + 128;
-  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::RING + C::SCALES);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(sb + 128 + BN);
   uint64_t* full = bars;
-  uint64_t* empty = bars + C::STAGES;
-  uint64_t* done = bars + 2 * C::STAGES;
+  uint64_t* empty = bars + C::DEEP;
+  uint64_t* done = bars + 2 * C::DEEP;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(done + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
@@ -96,16 +100,22 @@ __global__ void __launch_bounds__(kThreads)
   const int lb = tile % p.lane_tiles, cb = tile / p.lane_tiles;
   const int s0 = (int)((int64_t)p.k_tiles * split / splits), s1 = (int)((int64_t)p.k_tiles * (split + 1) / splits);
 
+  const int first = min(p.stages, s1 - s0);   // the first round of the ring
   if (threadIdx.x == 0) {
-    for (int s = 0; s < C::STAGES; ++s) {
+    for (int s = 0; s < p.stages; ++s) {
       tc::mbar_init(&full[s], 1);
       tc::mbar_init(&empty[s], 1);
     }
     tc::mbar_init(done, 1);
     *abort_flag = 0;
     tc::fence_barrier_init();
-    tc::prefetch_tensormap(&mapA);
-    tc::prefetch_tensormap(&mapB);
+    // the first loads leave before the other threads are ready; B's also under the tail of the
+    // preceding kernel
+    for (int s = 0; s < first; ++s) {
+      tc::mbar_expect_tx(&full[s], C::STAGE_BYTES);
+      tc::tma_load_2d(smem + s * C::STAGE_BYTES + C::A_BYTES, &mapB, &full[s], (s0 + s) * 128, lb * 128);
+      if (!p.early) tc::tma_load_2d(smem + s * C::STAGE_BYTES, &mapA, &full[s], (s0 + s) * 128, cb * BN);
+    }
   }
   if (warp == 1) {
     tc::tmem_alloc(tmem_slot, C::TMEM_COLS);
@@ -118,20 +128,13 @@ __global__ void __launch_bounds__(kThreads)
 
   if (warp == 0) {
     if (lane == 0) {
-      // the first round of the ring; B's tiles may go out under the tail of the preceding kernel
-      const int first = min(C::STAGES, s1 - s0);
-      for (int s = 0; s < first; ++s) {
-        tc::mbar_expect_tx(&full[s], C::STAGE_BYTES);
-        tc::tma_load_2d(smem + s * C::STAGE_BYTES + C::A_BYTES, &mapB, &full[s], (s0 + s) * 128, lb * 128);
-        if (!p.early) tc::tma_load_2d(smem + s * C::STAGE_BYTES, &mapA, &full[s], (s0 + s) * 128, cb * BN);
-      }
       if (p.early) {
         tc::grid_dependency_wait();
         for (int s = 0; s < first; ++s)
           tc::tma_load_2d(smem + s * C::STAGE_BYTES, &mapA, &full[s], (s0 + s) * 128, cb * BN);
       }
-      int stage = first == C::STAGES ? 0 : first, issued = first;
-      uint32_t phase = first == C::STAGES ? 1u : 0u;
+      int stage = first == p.stages ? 0 : first, issued = first;
+      uint32_t phase = first == p.stages ? 1u : 0u;
       for (int kk = s0 + first; kk < s1; ++kk) {
         if (!tc::mbar_wait(&empty[stage], phase ^ 1u, abort_flag)) {
           *abort_flag = 1;
@@ -142,16 +145,16 @@ __global__ void __launch_bounds__(kThreads)
         tc::mbar_expect_tx(&full[stage], C::STAGE_BYTES);
         tc::tma_load_2d(at + C::A_BYTES, &mapB, &full[stage], kk * 128, lb * 128);
         tc::tma_load_2d(at, &mapA, &full[stage], kk * 128, cb * BN);
-        if (++stage == C::STAGES) {
+        if (++stage == p.stages) {
           stage = 0;
           phase ^= 1u;
         }
         ++issued;
       }
       // after a timeout too, no load is in flight when the block goes on
-      for (int k = min(issued, C::STAGES); k > 0; --k) {
+      for (int k = min(issued, p.stages); k > 0; --k) {
         if (--stage < 0) {
-          stage = C::STAGES - 1;
+          stage = p.stages - 1;
           phase ^= 1u;
         }
         tc::mbar_wait(&full[stage], phase, nullptr);
@@ -175,7 +178,7 @@ __global__ void __launch_bounds__(kThreads)
 #pragma unroll
         for (int j = 0; j < 4; ++j) tc::mma_i8(tmem, lanes + 2 * j, cols + 2 * j, id, (kk != s0 || j) ? 1u : 0u);
         tc::tc_commit(&empty[stage]);
-        if (++stage == C::STAGES) {
+        if (++stage == p.stages) {
           stage = 0;
           phase ^= 1u;
         }
@@ -224,46 +227,35 @@ __global__ void __launch_bounds__(kThreads)
     tc::tmem_dealloc(tmem, C::TMEM_COLS);
   }
   // This CTA's part of the tile: runs of 8 columns of C, a 16-byte store of bf16 or two of fp32.
+  // Kept small (one output type, not unrolled): a CTA runs it once, and unrolled four times its
+  // instructions took 0.5 us longer to come in than they saved.
   if (warp >= 2) {
     constexpr int RUNS = 128 / 8;
-    const int64_t r0 = (int64_t)cb * BN, c0 = (int64_t)lb * 128;
+    const int rows = (int)min((int64_t)BN, p.p - (int64_t)cb * BN), cols = (int)min((int64_t)128, p.q - (int64_t)lb * 128);
+    OUT* const c0 = static_cast<OUT*>(p.C) + (int64_t)cb * BN * p.ldc + (int64_t)lb * 128;
     const uint32_t mine = tc::smem_addr(staged);
-    const int u1 = BN * RUNS * (split + 1) / splits;
-    for (int u = BN * RUNS * split / splits + (int)threadIdx.x - 64; u < u1; u += kThreads - 64) {
-      const int64_t i = r0 + u / RUNS, j = c0 + (u % RUNS) * 8;
-      if (i >= p.p || j >= p.q) continue;
-      const uint32_t off = (uint32_t)((u / RUNS) * C::PITCH + (u % RUNS) * 8) * 4u;
-      int acc[8] = {};
-      if (splits == 1) {
-        const int4 a = *reinterpret_cast<const int4*>(smem + off), b = *reinterpret_cast<const int4*>(smem + off + 16);
-        acc[0] = a.x; acc[1] = a.y; acc[2] = a.z; acc[3] = a.w;
-        acc[4] = b.x; acc[5] = b.y; acc[6] = b.z; acc[7] = b.w;
-      } else {
-        for (int s = 0; s < splits; ++s) {
-          const uint32_t from = tc::cluster_addr_u32(mine + off, (uint32_t)s);
-          const int4 a = load_cluster_int4(from), b = load_cluster_int4(from + 16);
-          acc[0] += a.x; acc[1] += a.y; acc[2] += a.z; acc[3] += a.w;
-          acc[4] += b.x; acc[5] += b.y; acc[6] += b.z; acc[7] += b.w;
-        }
+    const int u1 = rows * RUNS * (split + 1) / splits;
+    for (int u = rows * RUNS * split / splits + (int)threadIdx.x - 64; u < u1; u += kThreads - 64) {
+      const int i = u / RUNS, j = (u % RUNS) * 8;
+      if (j >= cols) continue;
+      const uint32_t off = (uint32_t)(i * C::PITCH + j) * 4u;
+      int4 a = make_int4(0, 0, 0, 0), b = a;
+      for (int s = 0; s < splits; ++s) {
+        const uint32_t from = tc::cluster_addr_u32(mine + off, (uint32_t)s);
+        const int4 x = load_cluster_int4(from), y = load_cluster_int4(from + 16);
+        a.x += x.x; a.y += x.y; a.z += x.z; a.w += x.w;
+        b.x += y.x; b.y += y.y; b.z += y.z; b.w += y.w;
       }
-      const float si = sa[u / RUNS];
-      const bool whole = j + 8 <= p.q;
-      float o[8];
-#pragma unroll
-      for (int e = 0; e < 8; ++e) o[e] = (float)acc[e] * si * sb[(u % RUNS) * 8 + e];
-      if (p.f32) {
-        float* dst = static_cast<float*>(p.C) + i * p.ldc + j;
-        if (whole) {
+      const float si = sa[i];
+      const float4 t0 = *reinterpret_cast<const float4*>(sb + j), t1 = *reinterpret_cast<const float4*>(sb + j + 4);
+      const float o[8] = {(float)a.x * si * t0.x, (float)a.y * si * t0.y, (float)a.z * si * t0.z, (float)a.w * si * t0.w,
+                          (float)b.x * si * t1.x, (float)b.y * si * t1.y, (float)b.z * si * t1.z, (float)b.w * si * t1.w};
+      OUT* dst = c0 + (int64_t)i * p.ldc + j;
+      if (j + 8 <= cols) {
+        if constexpr (sizeof(OUT) == 4) {
           *reinterpret_cast<float4*>(dst) = make_float4(o[0], o[1], o[2], o[3]);
           *reinterpret_cast<float4*>(dst + 4) = make_float4(o[4], o[5], o[6], o[7]);
         } else {
-#pragma unroll
-          for (int e = 0; e < 8; ++e)
-            if (j + e < p.q) dst[e] = o[e];
-        }
-      } else {
-        __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(p.C) + i * p.ldc + j;
-        if (whole) {
           uint32_t w[4];
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
@@ -271,11 +263,11 @@ __global__ void __launch_bounds__(kThreads)
             w[e] = *reinterpret_cast<const uint32_t*>(&pr);
           }
           *reinterpret_cast<uint4*>(dst) = make_uint4(w[0], w[1], w[2], w[3]);
-        } else {
-#pragma unroll
-          for (int e = 0; e < 8; ++e)
-            if (j + e < p.q) dst[e] = __float2bfloat16_rn(o[e]);
         }
+      } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          if (j + e < cols) dst[e] = (OUT)o[e];
       }
     }
   }
@@ -539,7 +531,7 @@ bool make_map_i8(CUtensorMap* map, const metis_int8* t, uint32_t box_rows) {
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int BN>
+template <int BN, typename OUT>
 metis_status launch_tile(metis_ctx* ctx, const metis_int8* A, const metis_int8* B, Params prm, int splits, bool chained) {
   using C = Cfg<BN>;
   CUtensorMap ma, mb;
@@ -549,14 +541,16 @@ metis_status launch_tile(metis_ctx* ctx, const metis_int8* A, const metis_int8* 
   const int64_t ctas = lane_tiles * col_tiles * splits;
   if (ctas > INT32_MAX) return fail(ctx, METIS_ERR_SHAPE, "too many output tiles");
   prm.lane_tiles = (int)lane_tiles;
-  auto kern = gemm_i8_kernel<BN>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::SMEM);
+  prm.stages = std::min(splits == 1 && ctas <= ctx->sm_count ? C::DEEP : C::STAGES, (prm.k_tiles + splits - 1) / splits);
+  const size_t smem = C::smem(prm.stages);
+  auto kern = gemm_i8_kernel<BN, OUT>;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return check_cuda(ctx, e, "cudaFuncSetAttribute(int8 gemm)");
   prm.early = chained;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3((unsigned)ctas);
   cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = C::SMEM;
+  cfg.dynamicSmemBytes = smem;
   cfg.stream = ctx->stream;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -629,9 +623,13 @@ metis_status launch_gemm_i8(metis_ctx* ctx, const metis_int8* A, const metis_int
   // 512 x 2304 x 768: 9.6, 9.1 in two, 10.0 in three).
   const int64_t room = (bn == 16 ? ctx->sm_count * 27 / 10 : ctx->sm_count) / tiles;
   const int splits = (int)std::max<int64_t>(1, std::min<int64_t>({8, room, prm.k_tiles / (bn == 16 ? 4 : 8)}));
-  if (bn == 16) return launch_tile<16>(ctx, A, B, prm, splits, chained);
-  if (bn == 32) return launch_tile<32>(ctx, A, B, prm, splits, chained);
-  return launch_tile<64>(ctx, A, B, prm, splits, chained);
+  auto launch = [&](auto zero) {
+    using OUT = decltype(zero);
+    if (bn == 16) return launch_tile<16, OUT>(ctx, A, B, prm, splits, chained);
+    if (bn == 32) return launch_tile<32, OUT>(ctx, A, B, prm, splits, chained);
+    return launch_tile<64, OUT>(ctx, A, B, prm, splits, chained);
+  };
+  return prm.f32 ? launch(float{}) : launch(__nv_bfloat16{});
 }
 
 }  // namespace metis
