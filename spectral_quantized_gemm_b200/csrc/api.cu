@@ -688,7 +688,7 @@ metis_status metis_quantize_int8(metis_ctx* ctx, const void* M, int64_t rows, in
     const metis_status s = check_quantize_int8(ctx, M, rows, cols, ld, dtype, rowwise, colwise);
     if (s != METIS_OK) return s;
     return check_cuda(ctx, launch_quantize_i8(M, dtype == METIS_OUT_BF16, rows, cols, ld, rowwise, colwise, ctx->status,
-                                              ctx->stream),
+                                              ctx->sm_count, ctx->stream),
                       "int8 quantize launch");
   });
 }
@@ -710,7 +710,7 @@ metis_status metis_linear_int8(metis_ctx* ctx, const void* X, int64_t ld, int32_
     metis_status s = check_quantize_int8(ctx, X, Xq->outer, Xq->inner, ld, dtype, Xq, nullptr);
     if (s != METIS_OK || (s = check_gemm_int8(ctx, Xq, W, C, ldc, c_dtype)) != METIS_OK) return s;
     s = check_cuda(ctx, launch_quantize_i8(X, dtype == METIS_OUT_BF16, Xq->outer, Xq->inner, ld, Xq, nullptr,
-                                           ctx->status, ctx->stream),
+                                           ctx->status, ctx->sm_count, ctx->stream),
                    "int8 quantize launch");
     return s == METIS_OK ? launch_gemm_i8(ctx, Xq, W, C, ldc, c_dtype, true) : s;
   });

@@ -172,7 +172,7 @@ metis_status run_lora_realign(metis_ctx* ctx, float* W, int64_t m, int64_t n, in
 // ---- quantize_i8.cu ----
 // Codes and scales of the rows (row, nullable) and of the columns (col, nullable, transposed).
 cudaError_t launch_quantize_i8(const void* M, bool bf16, int64_t rows, int64_t cols, int64_t ld, const metis_int8* row,
-                               const metis_int8* col, uint32_t* status, cudaStream_t st);
+                               const metis_int8* col, uint32_t* status, int sm_count, cudaStream_t st);
 // ---- gemm_i8.cu ----
 // chained: the launch before it on the stream is the quantizer that wrote A, itself an ordinary
 // launch, so that B is complete when this kernel starts early.
