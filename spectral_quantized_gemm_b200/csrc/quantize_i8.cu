@@ -136,15 +136,23 @@ __device__ __forceinline__ uint32_t chunk_finite_top(const Chunk<T>& k, uint32_t
 
 // The eight codes of a chunk under one scale, packed.
 template <typename T>
+__device__ __noinline__ uint2 chunk_codes_exact(Chunk<T> k, float a, float inv) {
+  uint32_t b[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) b[i] = (uint32_t)code_exact(k.get(i), a, inv);
+  return make_uint2(pack4(b[0], b[1], b[2], b[3]), pack4(b[4], b[5], b[6], b[7]));
+}
+__device__ __noinline__ uint32_t four_codes_exact(float x0, float x1, float x2, float x3, float a, float inv) {
+  return pack4((uint32_t)code_exact(x0, a, inv), (uint32_t)code_exact(x1, a, inv), (uint32_t)code_exact(x2, a, inv),
+               (uint32_t)code_exact(x3, a, inv));
+}
+template <typename T>
 __device__ __forceinline__ uint2 chunk_codes(const Chunk<T>& k, const LineScale& s) {
   uint32_t b[8];
   bool near = s.a < 0.0f;
 #pragma unroll
   for (int i = 0; i < 8; ++i) b[i] = code_bits<T>(k.get(i), s, near);
-  if (near) {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) b[i] = (uint32_t)code_exact(k.get(i), fabsf(s.a), s.inv);
-  }
+  if (near) return chunk_codes_exact(k, fabsf(s.a), s.inv);
   return make_uint2(pack4(b[0], b[1], b[2], b[3]), pack4(b[4], b[5], b[6], b[7]));
 }
 
@@ -160,19 +168,22 @@ __device__ __forceinline__ void store_codes(int8_t* row, int64_t c, int64_t cols
 }
 
 // ---------------------------------------------------------------- rows
-// GROUP threads take a row and hold it, CH chunks each, between the maximum and the codes, so
-// it is read once: a warp a row (8 rows a block), or a block a row where rows are long or
-// few.  CH = 0: a row too long for that is read again, from L2.
-template <typename T, int GROUP, int CH>
-__global__ void __launch_bounds__(kThreads) quantize_i8_rows_kernel(const T* __restrict__ M, int64_t rows, int64_t cols,
-                                                                    int64_t ld, int8_t* __restrict__ codes, int64_t ldq,
-                                                                    float* __restrict__ scales, uint32_t* status) {
-  __shared__ uint32_t part[2][kThreads / 32];
+// GROUP threads take a row and hold it, four chunks each at most, between the maximum and the
+// codes, so it is read once.  HELD false: a row too long for that is read again, from L2.
+// (A warp a row with 16 chunks each took 128 registers, a quarter of the SM's warps, and 27 us at
+// 8192 x 4096 bf16.)
+constexpr int kHeld = 4;
+
+template <typename T, int GROUP, bool HELD>
+__global__ void __launch_bounds__(GROUP > kThreads ? GROUP : kThreads)
+    quantize_i8_rows_kernel(const T* __restrict__ M, int64_t rows, int64_t cols, int64_t ld, int8_t* __restrict__ codes,
+                            int64_t ldq, float* __restrict__ scales, uint32_t* status) {
+  constexpr int BLOCK = GROUP > kThreads ? GROUP : kThreads;
+  __shared__ uint32_t part[2][BLOCK / 32];
   tc::grid_launch_dependents();   // a product that follows may start loading its other operand
   const int t = threadIdx.x % GROUP;
-  const int64_t r = (int64_t)blockIdx.x * (kThreads / GROUP) + threadIdx.x / GROUP;
-  if (GROUP == 32 && r >= rows) return;
-  const T* row = M + r * ld;
+  const int64_t r = (int64_t)blockIdx.x * (BLOCK / GROUP) + threadIdx.x / GROUP;
+  const T* row = M + min(r, rows - 1) * ld;   // a group past the last row repeats it and writes nothing
   int8_t* out = codes + r * ldq;
   const bool vec = (reinterpret_cast<uintptr_t>(row) & 15u) == 0;
 
@@ -182,36 +193,38 @@ __global__ void __launch_bounds__(kThreads) quantize_i8_rows_kernel(const T* __r
       if ((threadIdx.x & 31) == 0) part[slot][threadIdx.x >> 5] = top;
       __syncthreads();
 #pragma unroll
-      for (int i = 0; i < GROUP / 32; ++i) top = max(top, part[slot][i]);
+      for (int i = 0; i < GROUP / 32; ++i) top = max(top, part[slot][(threadIdx.x / GROUP) * (GROUP / 32) + i]);
     }
     return top;
   };
 
   uint32_t top = 0;
-  Chunk<T> held[CH > 0 ? CH : 1];
-  if constexpr (CH > 0) {
+  Chunk<T> held[kHeld];
+  if constexpr (HELD) {
 #pragma unroll
-    for (int i = 0; i < CH; ++i) held[i] = load_chunk(row, (int64_t)(i * GROUP + t) * 8, cols, vec);
+    for (int i = 0; i < kHeld; ++i) held[i] = load_chunk(row, (int64_t)(i * GROUP + t) * 8, cols, vec);
 #pragma unroll
-    for (int i = 0; i < CH; ++i) top = chunk_top(held[i], top);
+    for (int i = 0; i < kHeld; ++i) top = chunk_top(held[i], top);
   } else {
     for (int64_t c = (int64_t)t * 8; c < cols; c += GROUP * 8) top = chunk_top(load_chunk(row, c, cols, vec), top);
   }
   top = over_row(top, 0);
   const bool bad = top >= kInf;
-  if (bad) {
-    top = 0;
-    for (int64_t c = (int64_t)t * 8; c < cols; c += GROUP * 8) top = chunk_finite_top(load_chunk(row, c, cols, vec), top);
-    top = over_row(top, 1);
+  if (__syncthreads_or(bad)) {
+    uint32_t fine = 0;
+    for (int64_t c = (int64_t)t * 8; c < cols; c += GROUP * 8) fine = chunk_finite_top(load_chunk(row, c, cols, vec), fine);
+    fine = over_row(fine, 1);
+    if (bad) top = fine;
   }
+  if (r >= rows) return;
   const LineScale s = line_scale(top, bad);
   if (t == 0) {
     scales[r] = scale_of(s);
     if (bad) raise_status(status, METIS_DEV_NONFINITE);
   }
-  if constexpr (CH > 0) {
+  if constexpr (HELD) {
 #pragma unroll
-    for (int i = 0; i < CH; ++i) {
+    for (int i = 0; i < kHeld; ++i) {
       const int64_t c = (int64_t)(i * GROUP + t) * 8;
       if (c < cols) store_codes(out, c, cols, chunk_codes(held[i], s));
     }
@@ -235,7 +248,7 @@ __global__ void __launch_bounds__(kThreads) quantize_i8_cols_kernel(const T* __r
   __shared__ uint32_t part[kThreads / 32][kStrip];
   __shared__ uint32_t tops[2][kStrip];
   __shared__ LineScale line[kStrip];
-  __shared__ uint32_t tile[kStrip][kSlab / 4 + 1];   // four rows of a column in each word
+  __shared__ uint32_t tile[2][kStrip][kSlab / 4 + 1];   // four rows of a column in each word
   const int share = (int)tc::cluster_rank(), shares = (int)tc::cluster_size();
   const int64_t c0 = (int64_t)(blockIdx.x / shares) * kStrip;
   const int64_t slabs = (rows + kSlab - 1) / kSlab;
@@ -244,24 +257,48 @@ __global__ void __launch_bounds__(kThreads) quantize_i8_cols_kernel(const T* __r
   const int chunk = threadIdx.x & 7, group = threadIdx.x >> 3;   // 8 columns, 4 rows
   const int64_t c = c0 + chunk * 8;
   const bool vec = ((reinterpret_cast<uintptr_t>(M) | (uintptr_t)(ld * (int64_t)sizeof(T))) & 15u) == 0;
+  auto load_slab = [&](int64_t s, Chunk<T> (&k)[4]) {
+    const int64_t r0 = s * kSlab + group * 4;
+    const T* at = M + r0 * ld;
+    if (r0 + 4 <= rows) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i, at += ld) k[i] = load_chunk(at, c, cols, vec);
+    } else {   // the last row again does not change a maximum, and its codes are not written
+#pragma unroll
+      for (int i = 0; i < 4; ++i) k[i] = load_chunk(M + min(r0 + i, rows - 1) * ld, c, cols, vec);
+    }
+  };
 
   // Maxima of the strip's columns over all rows, in shared memory of every block.
   auto column_tops = [&](bool finite_only, int slot) {
     uint32_t top[8] = {};
-    for (int64_t s = first; s < last; ++s) {
-      Chunk<T> k[4];
+    if (sizeof(T) == 2 && !finite_only) {
+      uint32_t two[4] = {};
+      for (int64_t s = first; s < last; ++s) {
+        Chunk<T> k[4];
+        load_slab(s, k);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int64_t r = s * kSlab + group * 4 + i;
-        k[i] = load_chunk(M + min(r, rows - 1) * ld, c, cols, vec);   // a row again does not change a maximum
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) two[j] = __vmaxu2(two[j], k[i].w[j] & 0x7FFF7FFFu);
       }
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
+      for (int j = 0; j < 4; ++j) {
+        top[2 * j] = two[j] << 16;
+        top[2 * j + 1] = two[j] & 0xFFFF0000u;
+      }
+    } else {
+      for (int64_t s = first; s < last; ++s) {
+        Chunk<T> k[4];
+        load_slab(s, k);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const uint32_t b = __float_as_uint(k[i].get(j)) & 0x7FFFFFFFu;
-          if (!finite_only || b < kInf) top[j] = max(top[j], b);
-        }
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            const uint32_t b = __float_as_uint(k[i].get(j)) & 0x7FFFFFFFu;
+            if (!finite_only || b < kInf) top[j] = max(top[j], b);
+          }
+      }
     }
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
@@ -305,71 +342,61 @@ __global__ void __launch_bounds__(kThreads) quantize_i8_cols_kernel(const T* __r
 #pragma unroll
   for (int j = 0; j < 8; ++j) ls[j] = line[chunk * 8 + j];
 
-  for (int64_t s = first; s < last; ++s) {
+  int buf = 0;
+  for (int64_t s = first; s < last; ++s, buf ^= 1) {
     const int64_t r0 = s * kSlab;
     Chunk<T> k[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) k[i] = load_chunk(M + min(r0 + group * 4 + i, rows - 1) * ld, c, cols, vec);
+    load_slab(s, k);
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
       uint32_t b[4];
       bool near = ls[j].a < 0.0f;
 #pragma unroll
       for (int i = 0; i < 4; ++i) b[i] = code_bits<T>(k[i].get(j), ls[j], near);
-      if (near) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) b[i] = (uint32_t)code_exact(k[i].get(j), fabsf(ls[j].a), ls[j].inv);
-      }
-      tile[chunk * 8 + j][group] = pack4(b[0], b[1], b[2], b[3]);
+      uint32_t w = pack4(b[0], b[1], b[2], b[3]);
+      if (near) w = four_codes_exact(k[0].get(j), k[1].get(j), k[2].get(j), k[3].get(j), fabsf(ls[j].a), ls[j].inv);
+      tile[buf][chunk * 8 + j][group] = w;
     }
-    __syncthreads();
+    __syncthreads();   // the other buffer was read before the block came here
     // 16 rows (16 bytes) of a column per thread and step
 #pragma unroll
     for (int u = threadIdx.x; u < kStrip * 8; u += kThreads) {
       const int64_t cc = c0 + (u >> 3), rr = r0 + (u & 7) * 16;
       if (cc >= cols || rr >= rows) continue;
-      uint32_t w[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) w[i] = tile[u >> 3][(u & 7) * 4 + i];
+      const uint32_t* from = &tile[buf][u >> 3][(u & 7) * 4];
       int8_t* dst = codes + cc * ldq + rr;
       if (rr + 16 <= rows) {
-        *reinterpret_cast<uint4*>(dst) = make_uint4(w[0], w[1], w[2], w[3]);
+        *reinterpret_cast<uint4*>(dst) = make_uint4(from[0], from[1], from[2], from[3]);
       } else {
-#pragma unroll
-        for (int i = 0; i < 16; ++i)
-          if (rr + i < rows) dst[i] = (int8_t)(w[i >> 2] >> (8 * (i & 3)));
+        for (int i = 0; rr + i < rows; ++i) dst[i] = (int8_t)(from[i >> 2] >> (8 * (i & 3)));
       }
     }
-    __syncthreads();
   }
   tc::cluster_wait();                          // nor does a block leave while its own are read
   tc::grid_dependency_wait();                  // the row kernel before this one, beside which it ran
 }
 
-template <typename T, int GROUP, int CH>
+template <typename T, int GROUP, bool HELD>
 cudaError_t launch_rows(const T* M, int64_t rows, int64_t cols, int64_t ld, const metis_int8* q, uint32_t* status,
                         cudaStream_t st) {
-  const int64_t blocks = (rows * GROUP + kThreads - 1) / kThreads;
-  quantize_i8_rows_kernel<T, GROUP, CH><<<(unsigned)blocks, kThreads, 0, st>>>(M, rows, cols, ld, q->codes, q->ld, q->scales, status);
+  constexpr int BLOCK = GROUP > kThreads ? GROUP : kThreads;
+  const int64_t blocks = (rows + BLOCK / GROUP - 1) / (BLOCK / GROUP);
+  quantize_i8_rows_kernel<T, GROUP, HELD><<<(unsigned)blocks, BLOCK, 0, st>>>(M, rows, cols, ld, q->codes, q->ld, q->scales, status);
   count_launch();
   return cudaGetLastError();
 }
 
+// The smallest group that holds a row; where rows are too few to fill the SMs, the largest that
+// has a chunk for each thread.
 template <typename T>
 cudaError_t run_rows(const T* M, int64_t rows, int64_t cols, int64_t ld, const metis_int8* q, uint32_t* status, int sm_count,
                      cudaStream_t st) {
   const int64_t chunks = (cols + 7) / 8;
-  constexpr int kMost = sizeof(T) == 2 ? 16 : 8;   // chunks that a thread holds: 64 registers
-  if (rows >= 8 * (int64_t)sm_count && chunks <= 32 * kMost) {
-    if (chunks <= 32 * 2) return launch_rows<T, 32, 2>(M, rows, cols, ld, q, status, st);
-    if (chunks <= 32 * 4) return launch_rows<T, 32, 4>(M, rows, cols, ld, q, status, st);
-    if (chunks <= 32 * 8) return launch_rows<T, 32, 8>(M, rows, cols, ld, q, status, st);
-    return launch_rows<T, 32, kMost>(M, rows, cols, ld, q, status, st);
-  }
-  if (chunks <= kThreads) return launch_rows<T, kThreads, 1>(M, rows, cols, ld, q, status, st);
-  if (chunks <= kThreads * 2) return launch_rows<T, kThreads, 2>(M, rows, cols, ld, q, status, st);
-  if (chunks <= kThreads * 8) return launch_rows<T, kThreads, 8>(M, rows, cols, ld, q, status, st);
-  return launch_rows<T, kThreads, 0>(M, rows, cols, ld, q, status, st);
+  if (chunks > 512 * kHeld) return launch_rows<T, 512, false>(M, rows, cols, ld, q, status, st);
+  const bool few = rows < 4 * (int64_t)sm_count;
+  if (few ? chunks <= 64 : chunks <= 32 * kHeld) return launch_rows<T, 32, true>(M, rows, cols, ld, q, status, st);
+  if (few ? chunks <= 256 : chunks <= 128 * kHeld) return launch_rows<T, 128, true>(M, rows, cols, ld, q, status, st);
+  return launch_rows<T, 512, true>(M, rows, cols, ld, q, status, st);
 }
 
 // beside: the launch before this one on the stream is the row kernel of the same matrix (an
