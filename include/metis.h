@@ -339,22 +339,26 @@ metis_status metis_lora_realign(metis_ctx* ctx, float* W_res, int64_t m, int64_t
  * the product that reads it.  codes 16-byte aligned, ld >= inner and a multiple of 16;
  * the bytes from inner to ld of a line are neither read nor written.  Unlike the NVFP4
  * operands these have no limits on outer and inner besides 1 <= outer, inner < 2^31.
+ * scratch: 2 * outer words that a column-wise quantization into this tensor overwrites (it
+ * gathers the maxima there); may be NULL in every other use.
  */
 typedef struct {
   int8_t* codes;
   float* scales;
   int64_t outer, inner, ld;
+  uint32_t* scratch;
 } metis_int8;
 
 /*
  * 8-bit quantization of a device matrix M (rows x cols, leading dimension ld >= cols,
  * dtype METIS_OUT_F32 or METIS_OUT_BF16, aligned to its element), round to nearest:
  *   rowwise (nullable): outer = rows, inner = cols, a scale for each row (token)
- *   colwise (nullable): outer = cols, inner = rows, a scale for each column (channel); M^T
+ *   colwise (nullable): outer = cols, inner = rows, a scale for each column (channel); M^T;
+ *     needs its scratch
  * For a line with amax = max |x| over its finite entries and a = max(amax, 127 * 2^-126):
  * scale = fp32(a / 127), code = 127 x / a rounded to the nearest integer, ties to even,
  * decided on the exact quotient.  A line of zeros has zero codes.  NaN gives code 0, an
- * infinity +-127; device: METIS_DEV_NONFINITE for both.  No workspace.
+ * infinity +-127; device: METIS_DEV_NONFINITE for both.  No context workspace.
  */
 metis_status metis_quantize_int8(metis_ctx* ctx, const void* M, int64_t rows, int64_t cols, int64_t ld, int32_t dtype,
                                  metis_int8* rowwise, metis_int8* colwise);

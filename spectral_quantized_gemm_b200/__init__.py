@@ -76,7 +76,8 @@ class QuantParams(ctypes.Structure):
 
 
 class Int8Struct(ctypes.Structure):
-    _fields_ = [("codes", c_p), ("scales", c_p), ("outer", c_i64), ("inner", c_i64), ("ld", c_i64)]
+    _fields_ = [("codes", c_p), ("scales", c_p), ("outer", c_i64), ("inner", c_i64), ("ld", c_i64),
+                ("scratch", c_p)]
 
 
 class AdamWTensor(ctypes.Structure):
@@ -229,7 +230,14 @@ class Int8:
         # the row stride of a single row says nothing and may be anything
         ld = codes.stride(0) if self.outer > 1 else -(-self.inner // 16) * 16
         self.codes, self.scales = codes, scales
-        self.struct = Int8Struct(codes.data_ptr(), scales.data_ptr(), self.outer, self.inner, ld)
+        self.scratch = None      # made when a column-wise quantization first needs it
+        self.struct = Int8Struct(codes.data_ptr(), scales.data_ptr(), self.outer, self.inner, ld, None)
+
+    def with_scratch(self):
+        if self.scratch is None:
+            self.scratch = torch.empty(2 * self.outer, dtype=torch.int32, device=self.codes.device)
+            self.struct.scratch = self.scratch.data_ptr()
+        return self
 
     def dequantize(self):
         """The decoded fp32 matrix (outer x inner)."""
@@ -425,7 +433,7 @@ class Context:
         ptr, ld, dtype = _dense(M, "M")
         self._call(_quant_i8, ptr, M.shape[0], M.shape[1], ld, dtype,
                    None if rowwise is None else ctypes.byref(rowwise.struct),
-                   None if colwise is None else ctypes.byref(colwise.struct))
+                   None if colwise is None else ctypes.byref(colwise.with_scratch().struct))
 
     def gemm_int8(self, A, B, C):
         """C[i, j] = (sum_k A[i, k] B[j, k]) A.scales[i] B.scales[j] (C fp32 or bf16)."""

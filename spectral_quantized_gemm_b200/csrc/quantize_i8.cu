@@ -7,18 +7,18 @@
 // METIS_DEV_NONFINITE).  The floor on a keeps the scale a normal number, also for a line
 // of zeros.
 //
-// The quotient.  127 / a is held in two fp32 words, inv + lo (lo is the rounded remainder of
-// the rounded quotient over a, so their sum is off by 2^-46 of it), and
+// The quotient.  127 / a is held in two fp32 words, inv from an approximate reciprocal r of a
+// (2^-22) and lo = (127 - inv a) r, so their sum is off by 2^-44 of it, and
 //   y = fma(x, inv, x lo)
-// is the fp32 number nearest to 127 x / a, up to 2^-24 of an ulp.  Adding 1.5 * 2^23 rounds
+// is the fp32 number nearest to 127 x / a, up to 2^-20 of an ulp.  Adding 1.5 * 2^23 rounds
 // it to an integer, ties to even, in the low byte.
 //   bf16 x: a quotient half way between two integers is itself an fp32 number, so y is that
 //     number; every other quotient of two 8-bit mantissas differs from such a border by
 //     2^-16 of itself or more (254 X - (2 n + 1) A is an integer), y by 2^-24.  y decides.
-//   fp32 x: where y lies within 2^-15 of a border, the two sides of 254 |x| <> (2 n + 1) a
-//     are compared in fp64, both exact (24 + 8 bits).  One element in 2^14.
-// Lines with a > 2^100 (lo would be subnormal) or with entries that are not finite take the
-// fp64 comparison for every element.
+//   fp32 x: where y lies within 2^-15 of a border (one element in 2^14), the two sides of
+//     254 |x| <> (2 n + 1) a are compared, each an fp32 product and its exact remainder.
+// Lines whose a lies outside 2^-90 .. 2^100 (a remainder could be subnormal) or with entries
+// that are not finite take a comparison in fp64 (24 + 8 bits: exact) for every element.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -43,9 +43,12 @@ struct LineScale {
 __device__ __forceinline__ LineScale line_scale(uint32_t amax_bits, bool nonfinite) {
   LineScale s;
   const float a = fmaxf(__uint_as_float(amax_bits), kMinAmax);
-  s.inv = __fdiv_rn(127.0f, a);
-  s.lo = __fdiv_rn(__fmaf_rn(-s.inv, a, 127.0f), a);
-  s.a = nonfinite || a > 1.2676506e30f ? -a : a;       // 2^100
+  float r;
+  asm("rcp.approx.f32 %0, %1;" : "=f"(r) : "f"(a));
+  s.inv = __fmul_rn(127.0f, r);
+  s.lo = __fmul_rn(__fmaf_rn(-s.inv, a, 127.0f), r);
+  // 2^100 and 2^-90; a line of zeros needs no comparison
+  s.a = nonfinite || a > 1.2676506e30f || (amax_bits != 0 && a < 8.0779357e-28f) ? -a : a;
   return s;
 }
 __device__ __forceinline__ float scale_of(const LineScale& s) { return __fdiv_rn(fabsf(s.a), 127.0f); }
@@ -54,7 +57,7 @@ __device__ __forceinline__ float scale_of(const LineScale& s) { return __fdiv_rn
 __device__ __noinline__ int code_exact(float x, float a, float inv) {
   if (!(x == x)) return 0;
   const double m = fmin(fabs((double)x), (double)a);   // an infinity saturates
-  const float y = fminf((float)m * inv, 127.0f);       // within 2^-16 of the quotient
+  const float y = fminf((float)m * inv, 127.0f);       // within 2^-14 of the quotient
   // the code is the number of borders (n + 1/2) below the quotient; y finds the nearest one
   const int n = (int)floorf(y);                         // the border n + 1/2, or one of its neighbours
   int c = max(n - 1, 0);
@@ -65,11 +68,20 @@ __device__ __noinline__ int code_exact(float x, float a, float inv) {
   return x < 0.0f ? -c : c;
 }
 
+// The code in the low byte, for a line that needs no fp64 comparison.
 template <typename T>
-__device__ __forceinline__ uint32_t code_bits(float x, const LineScale& s, bool& near) {
+__device__ __forceinline__ uint32_t code_bits(float x, const LineScale& s) {
   const float y = __fmaf_rn(x, s.inv, __fmul_rn(x, s.lo));
-  const float t = __fadd_rn(y, 12582912.0f);
-  if (sizeof(T) == 4) near |= fabsf(__fsub_rn(y, __fsub_rn(t, 12582912.0f))) > 0.49996f;
+  float t = __fadd_rn(y, 12582912.0f);
+  if constexpr (sizeof(T) == 4) {
+    if (fabsf(__fsub_rn(y, __fsub_rn(t, 12582912.0f))) > 0.49996f) {
+      const float m = fabsf(x), n = floorf(fabsf(y)), odd = 2.0f * n + 1.0f;
+      const float l = __fmul_rn(254.0f, m), r = __fmul_rn(odd, s.a);
+      const float d = __fadd_rn(__fsub_rn(l, r), __fsub_rn(__fmaf_rn(254.0f, m, -l), __fmaf_rn(odd, s.a, -r)));
+      const float c = n + (d > 0.0f || (d == 0.0f && ((int)n & 1)) ? 1.0f : 0.0f);
+      t = __fadd_rn(copysignf(c, x), 12582912.0f);
+    }
+  }
   return __float_as_uint(t);
 }
 
@@ -89,9 +101,9 @@ struct Chunk {
 
 // Elements from column c on; columns >= cols read as 0.  vec: the row starts on 16 bytes.
 template <typename T>
-__device__ __forceinline__ Chunk<T> load_chunk(const T* row, int64_t c, int64_t cols, bool vec) {
+__device__ __forceinline__ Chunk<T> load_chunk(const T* row, int c, int cols, bool vec) {
   Chunk<T> k;
-  if (vec && c + 8 <= cols) {
+  if (vec && c <= cols - 8) {
 #pragma unroll
     for (int i = 0; i < (int)sizeof(T) / 2; ++i) {
       const uint4 u = reinterpret_cast<const uint4*>(row + c)[i];
@@ -99,12 +111,12 @@ __device__ __forceinline__ Chunk<T> load_chunk(const T* row, int64_t c, int64_t 
     }
   } else if constexpr (sizeof(T) == 4) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) k.w[i] = c + i < cols ? reinterpret_cast<const uint32_t*>(row)[c + i] : 0u;
+    for (int i = 0; i < 8; ++i) k.w[i] = c < cols - i ? reinterpret_cast<const uint32_t*>(row)[c + i] : 0u;
   } else {
     const uint16_t* h = reinterpret_cast<const uint16_t*>(row);
 #pragma unroll
     for (int i = 0; i < 4; ++i)
-      k.w[i] = (c + 2 * i < cols ? (uint32_t)h[c + 2 * i] : 0u) | (c + 2 * i + 1 < cols ? (uint32_t)h[c + 2 * i + 1] << 16 : 0u);
+      k.w[i] = (c < cols - 2 * i ? (uint32_t)h[c + 2 * i] : 0u) | (c < cols - 2 * i - 1 ? (uint32_t)h[c + 2 * i + 1] << 16 : 0u);
   }
   return k;
 }
@@ -148,290 +160,358 @@ __device__ __noinline__ uint32_t four_codes_exact(float x0, float x1, float x2, 
 }
 template <typename T>
 __device__ __forceinline__ uint2 chunk_codes(const Chunk<T>& k, const LineScale& s) {
+  if (s.a < 0.0f) return chunk_codes_exact(k, -s.a, s.inv);
   uint32_t b[8];
-  bool near = s.a < 0.0f;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) b[i] = code_bits<T>(k.get(i), s, near);
-  if (near) return chunk_codes_exact(k, fabsf(s.a), s.inv);
+  for (int i = 0; i < 8; ++i) b[i] = code_bits<T>(k.get(i), s);
   return make_uint2(pack4(b[0], b[1], b[2], b[3]), pack4(b[4], b[5], b[6], b[7]));
 }
 
 // Eight codes; the bytes of columns >= cols are not written.
-__device__ __forceinline__ void store_codes(int8_t* row, int64_t c, int64_t cols, uint2 w) {
-  if (c + 8 <= cols) {
+__device__ __forceinline__ void store_codes(int8_t* row, int c, int cols, uint2 w) {
+  if (c <= cols - 8) {
     *reinterpret_cast<uint2*>(row + c) = w;
   } else {
 #pragma unroll
     for (int i = 0; i < 8; ++i)
-      if (c + i < cols) row[c + i] = (int8_t)((i < 4 ? w.x : w.y) >> (8 * (i & 3)));
+      if (c < cols - i) row[c + i] = (int8_t)((i < 4 ? w.x : w.y) >> (8 * (i & 3)));
   }
 }
 
 // ---------------------------------------------------------------- rows
-// GROUP threads take a row and hold it, four chunks each at most, between the maximum and the
-// codes, so it is read once.  HELD false: a row too long for that is read again, from L2.
-// (A warp a row with 16 chunks each took 128 registers, a quarter of the SM's warps, and 27 us at
-// 8192 x 4096 bf16.)
+// GROUP threads take a row at a time and hold it, four chunks each at most, between the maximum
+// and the codes, so it is read once; the next row is loaded before the work on one begins
+// (without that a block waited for its loads most of the time: 21 us at 8192 x 4096 bf16, 19 with
+// it).  A block is one group, or eight where a group is a warp, and goes on to further rows.
+//   TOPS: a thread meets the same columns in every row, and gathers their maxima on the way;
+// they are joined in `tops` by integer atomicMax (the order does not matter), a warp's 32
+// neighbours at a time.  codes == nullptr: only that.
 constexpr int kHeld = 4;
 
-template <typename T, int GROUP, bool HELD>
-__global__ void __launch_bounds__(GROUP > kThreads ? GROUP : kThreads)
-    quantize_i8_rows_kernel(const T* __restrict__ M, int64_t rows, int64_t cols, int64_t ld, int8_t* __restrict__ codes,
-                            int64_t ldq, float* __restrict__ scales, uint32_t* status) {
-  constexpr int BLOCK = GROUP > kThreads ? GROUP : kThreads;
-  __shared__ uint32_t part[2][BLOCK / 32];
-  tc::grid_launch_dependents();   // a product that follows may start loading its other operand
-  const int t = threadIdx.x % GROUP;
-  const int64_t r = (int64_t)blockIdx.x * (BLOCK / GROUP) + threadIdx.x / GROUP;
-  const T* row = M + min(r, rows - 1) * ld;   // a group past the last row repeats it and writes nothing
-  int8_t* out = codes + r * ldq;
-  const bool vec = (reinterpret_cast<uintptr_t>(row) & 15u) == 0;
+// Column maxima of a thread's chunks: bf16 two to a word (their bits order like the values).
+template <typename T>
+struct ColumnTops {
+  static constexpr int WORDS = 2 * (int)sizeof(T);
+  uint32_t w[kHeld][WORDS];
+  __device__ __forceinline__ void add(int i, const Chunk<T>& k) {
+#pragma unroll
+    for (int j = 0; j < WORDS; ++j) {
+      if constexpr (sizeof(T) == 2) w[i][j] = __vmaxu2(w[i][j], k.w[j] & 0x7FFF7FFFu);
+      else w[i][j] = max(w[i][j], k.w[j] & 0x7FFFFFFFu);
+    }
+  }
+  __device__ __forceinline__ uint32_t get(int i, int j) const {   // fp32 bits
+    if constexpr (sizeof(T) == 4) return w[i][j];
+    else return (j & 1) ? w[i][j >> 1] & 0xFFFF0000u : w[i][j >> 1] << 16;
+  }
+};
 
-  auto over_row = [&](uint32_t top, int slot) {
+// A chunk with entries that are not finite: they are left out and their columns marked.
+template <typename T>
+__device__ __noinline__ Chunk<T> mark_nonfinite(Chunk<T> k, int c, uint32_t* marks, uint32_t* status) {
+#pragma unroll
+  for (int j = 0; j < 8; ++j)
+    if ((__float_as_uint(k.get(j)) & 0x7FFFFFFFu) >= kInf) {
+      marks[c + j] = 1;
+      if constexpr (sizeof(T) == 4) k.w[j] = 0;
+      else k.w[j >> 1] &= (j & 1) ? 0x0000FFFFu : 0xFFFF0000u;
+    }
+  raise_status(status, METIS_DEV_NONFINITE);
+  return k;
+}
+
+// Threads of an SM: what the registers allow.
+template <typename T, bool TOPS>
+constexpr int kRowThreads = (sizeof(T) == 2 ? 1024 : 640) - (TOPS ? (sizeof(T) == 2 ? 256 : 128) : 0);
+
+template <typename T, int GROUP, bool TOPS>
+__global__ void __launch_bounds__(GROUP == 32 ? kThreads : GROUP, kRowThreads<T, TOPS> / (GROUP == 32 ? kThreads : GROUP))
+    quantize_i8_rows_kernel(const T* __restrict__ M, int64_t rows, int cols, int64_t ld, int8_t* __restrict__ codes,
+                            int64_t ldq, float* __restrict__ scales, uint32_t* __restrict__ tops,
+                            uint32_t* __restrict__ marks, uint32_t* status) {
+  constexpr int BLOCK = GROUP == 32 ? kThreads : GROUP;
+  __shared__ uint32_t part[2][2][BLOCK / 32];
+  tc::grid_launch_dependents();   // what follows may start loading
+  const int t = threadIdx.x % GROUP;
+  const int64_t step = (int64_t)gridDim.x * (BLOCK / GROUP);
+  int64_t r = (int64_t)blockIdx.x * (BLOCK / GROUP) + threadIdx.x / GROUP;
+
+  auto load_row = [&](int64_t r, Chunk<T> (&k)[kHeld]) {
+    const T* row = M + r * ld;
+    const bool vec = (reinterpret_cast<uintptr_t>(row) & 15u) == 0;
+#pragma unroll
+    for (int i = 0; i < kHeld; ++i) k[i] = load_chunk(row, (i * GROUP + t) * 8, cols, vec);
+  };
+  auto over_row = [&](uint32_t top, uint32_t* slot) {
     top = __reduce_max_sync(0xffffffffu, top);
-    if (GROUP > 32) {
-      if ((threadIdx.x & 31) == 0) part[slot][threadIdx.x >> 5] = top;
+    if constexpr (GROUP > 32) {
+      if ((threadIdx.x & 31) == 0) slot[threadIdx.x >> 5] = top;
       __syncthreads();
 #pragma unroll
-      for (int i = 0; i < GROUP / 32; ++i) top = max(top, part[slot][(threadIdx.x / GROUP) * (GROUP / 32) + i]);
+      for (int i = 0; i < GROUP / 32; ++i) top = max(top, slot[i]);
     }
     return top;
   };
 
-  uint32_t top = 0;
-  Chunk<T> held[kHeld];
-  if constexpr (HELD) {
+  ColumnTops<T> col{};
+  Chunk<T> next[kHeld];
+  if (r < rows) load_row(r, next);
+  for (int turn = 0; r < rows; r += step, turn ^= 1) {
+    Chunk<T> held[kHeld];
 #pragma unroll
-    for (int i = 0; i < kHeld; ++i) held[i] = load_chunk(row, (int64_t)(i * GROUP + t) * 8, cols, vec);
+    for (int i = 0; i < kHeld; ++i) held[i] = next[i];
+    if (r + step < rows) load_row(r + step, next);
+    uint32_t top = 0;
 #pragma unroll
     for (int i = 0; i < kHeld; ++i) top = chunk_top(held[i], top);
-  } else {
-    for (int64_t c = (int64_t)t * 8; c < cols; c += GROUP * 8) top = chunk_top(load_chunk(row, c, cols, vec), top);
+    if constexpr (TOPS) {
+      if (top < kInf) {
+#pragma unroll
+        for (int i = 0; i < kHeld; ++i) col.add(i, held[i]);
+      } else {
+#pragma unroll
+        for (int i = 0; i < kHeld; ++i) col.add(i, mark_nonfinite(held[i], (i * GROUP + t) * 8, marks, status));
+      }
+      if (!codes) continue;
+    }
+    top = over_row(top, part[turn][0]);
+    const bool bad = top >= kInf;      // the same in the whole group
+    if (bad) {
+      top = 0;
+#pragma unroll
+      for (int i = 0; i < kHeld; ++i) top = chunk_finite_top(held[i], top);
+      top = over_row(top, part[turn][1]);
+    }
+    const LineScale s = line_scale(top, bad);
+    if (t == 0) {
+      scales[r] = scale_of(s);
+      if (bad) raise_status(status, METIS_DEV_NONFINITE);
+    }
+    int8_t* out = codes + r * ldq;
+#pragma unroll
+    for (int i = 0; i < kHeld; ++i) {
+      const int c = (i * GROUP + t) * 8;
+      if (c < cols) store_codes(out, c, cols, chunk_codes(held[i], s));
+    }
   }
-  top = over_row(top, 0);
+  if constexpr (TOPS) {
+    // lane l holds columns 8 l .. 8 l + 7 of 256; turned through shared memory, 32 neighbours at a time
+    __shared__ uint32_t turned[BLOCK / 32][32 * 9];
+    uint32_t* mine = turned[threadIdx.x >> 5];
+    const int lane = threadIdx.x & 31, warp_t = t & ~31;
+#pragma unroll
+    for (int i = 0; i < kHeld; ++i) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) mine[lane * 9 + j] = col.get(i, j);
+      __syncwarp();
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const int e = j * 32 + lane, c = (i * GROUP + warp_t) * 8 + e;
+        const uint32_t m = mine[(e >> 3) * 9 + (e & 7)];
+        if (c < cols && m) atomicMax(&tops[c], m);
+      }
+      __syncwarp();
+    }
+  }
+}
+
+// A row longer than a group holds: read twice, the second time from L2 if it fits there.
+template <typename T>
+__global__ void __launch_bounds__(512) quantize_i8_long_rows_kernel(const T* __restrict__ M, int cols, int64_t ld,
+                                                                    int8_t* __restrict__ codes, int64_t ldq,
+                                                                    float* __restrict__ scales, uint32_t* status) {
+  __shared__ uint32_t part[2][16];
+  tc::grid_launch_dependents();
+  const int64_t r = blockIdx.x;
+  const T* row = M + r * ld;
+  const bool vec = (reinterpret_cast<uintptr_t>(row) & 15u) == 0;
+  auto over_row = [&](bool finite_only) {
+    uint32_t top = 0;
+    for (uint32_t c = threadIdx.x * 8; c < (uint32_t)cols; c += 512 * 8) {
+      const Chunk<T> k = load_chunk(row, c, cols, vec);
+      top = finite_only ? chunk_finite_top(k, top) : chunk_top(k, top);
+    }
+    top = __reduce_max_sync(0xffffffffu, top);
+    if ((threadIdx.x & 31) == 0) part[finite_only][threadIdx.x >> 5] = top;
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < 16; ++i) top = max(top, part[finite_only][i]);
+    return top;
+  };
+  uint32_t top = over_row(false);
   const bool bad = top >= kInf;
-  if (__syncthreads_or(bad)) {
-    uint32_t fine = 0;
-    for (int64_t c = (int64_t)t * 8; c < cols; c += GROUP * 8) fine = chunk_finite_top(load_chunk(row, c, cols, vec), fine);
-    fine = over_row(fine, 1);
-    if (bad) top = fine;
-  }
-  if (r >= rows) return;
+  if (bad) top = over_row(true);
   const LineScale s = line_scale(top, bad);
-  if (t == 0) {
+  if (threadIdx.x == 0) {
     scales[r] = scale_of(s);
     if (bad) raise_status(status, METIS_DEV_NONFINITE);
   }
-  if constexpr (HELD) {
-#pragma unroll
-    for (int i = 0; i < kHeld; ++i) {
-      const int64_t c = (int64_t)(i * GROUP + t) * 8;
-      if (c < cols) store_codes(out, c, cols, chunk_codes(held[i], s));
-    }
-  } else {
-    for (int64_t c = (int64_t)t * 8; c < cols; c += GROUP * 8)
-      store_codes(out, c, cols, chunk_codes(load_chunk(row, c, cols, vec), s));
-  }
+  for (uint32_t c = threadIdx.x * 8; c < (uint32_t)cols; c += 512 * 8)
+    store_codes(codes + r * ldq, c, cols, chunk_codes(load_chunk(row, c, cols, vec), s));
 }
 
 // ---------------------------------------------------------------- columns
-// A cluster takes a strip of 64 columns, each of its blocks a share of the rows: maxima of
-// the share, joined through distributed shared memory, then the codes of the share in slabs
-// of 128 rows, transposed through shared memory so that a column leaves as 128 bytes.  The
-// second reading of a share finds it in L2 (the strips under way hold some 40 MB of its 126).
-constexpr int kStrip = 64, kSlab = 128;
+// The codes of the columns from their maxima: a tile of 128 bytes of 256 rows goes to shared
+// memory, all of it on its way at once (cp.async), also under the tail of the kernel that makes
+// the maxima.  Then a thread takes a word of a row (two columns bf16, one fp32) in 16
+// consecutive rows, so its codes are 16 bytes of a column each; the lanes of a warp are 4 words
+// by 8 such pieces, so a column leaves as 128 bytes.  16 bytes of padding after 16 rows keep
+// the pieces on different banks.  Tiles go from the last row to the first: the last rows read
+// before are what L2 still holds.
+//   (One reading instead of two, by clusters that keep strips of columns in shared memory while
+// their maxima are joined, took 36 us or more at 8192 x 4096 bf16 in all forms tried: a block
+// waited most of its time for the join.)
+constexpr int kPiece = 16, kTileRows = 256, kRowBytes = 128;
+constexpr int kPieceBytes = kPiece * kRowBytes + 16;
+
+__device__ __forceinline__ void copy_async16(void* dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(tc::smem_addr(dst)), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copy_async_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 
 template <typename T>
-__global__ void __launch_bounds__(kThreads) quantize_i8_cols_kernel(const T* __restrict__ M, int64_t rows, int64_t cols,
-                                                                    int64_t ld, int8_t* __restrict__ codes, int64_t ldq,
-                                                                    float* __restrict__ scales, uint32_t* status) {
-  __shared__ uint32_t part[kThreads / 32][kStrip];
-  __shared__ uint32_t tops[2][kStrip];
-  __shared__ LineScale line[kStrip];
-  __shared__ uint32_t tile[2][kStrip][kSlab / 4 + 1];   // four rows of a column in each word
-  const int share = (int)tc::cluster_rank(), shares = (int)tc::cluster_size();
-  const int64_t c0 = (int64_t)(blockIdx.x / shares) * kStrip;
-  const int64_t slabs = (rows + kSlab - 1) / kSlab;
-  const int64_t first = slabs * share / shares, last = slabs * (share + 1) / shares;
+__global__ void __launch_bounds__(kThreads, 5) quantize_i8_cols_kernel(const T* __restrict__ M, int64_t rows, int64_t cols,
+                                                                       int64_t ld, int8_t* __restrict__ codes, int64_t ldq,
+                                                                       float* __restrict__ scales, const uint32_t* tops,
+                                                                       const uint32_t* marks) {
+  constexpr int COLS = kRowBytes / (int)sizeof(T), PER_WORD = 4 / (int)sizeof(T);
+  __shared__ __align__(16) uint8_t data[kTileRows / kPiece * kPieceBytes];
+  const int64_t strips = (cols + COLS - 1) / COLS, c0 = (blockIdx.x % strips) * COLS;
+  const int64_t tile = (rows + kTileRows - 1) / kTileRows - 1 - blockIdx.x / strips, r0 = tile * kTileRows;
+  const int n = (int)min((int64_t)kTileRows, rows - r0);
+  const bool aligned = ((reinterpret_cast<uintptr_t>(M) | (uintptr_t)(ld * (int64_t)sizeof(T))) & 15u) == 0;
+  if (aligned && c0 + COLS <= cols) {
+    const int chunk = threadIdx.x & 7;
+    const T* src = M + (r0 + (threadIdx.x >> 3)) * ld + c0 + chunk * (16 / (int)sizeof(T));
+    for (int r = threadIdx.x >> 3; r < n; r += kThreads / 8, src += (kThreads / 8) * ld)
+      copy_async16(data + (r / kPiece) * kPieceBytes + (r % kPiece) * kRowBytes + chunk * 16, src);
+  } else {
+    for (int e = threadIdx.x; e < n * COLS; e += kThreads) {
+      const int r = e / COLS, j = e % COLS;
+      if (c0 + j < cols)
+        *(reinterpret_cast<T*>(data + (r / kPiece) * kPieceBytes + (r % kPiece) * kRowBytes) + j) = M[(r0 + r) * ld + c0 + j];
+    }
+  }
+  tc::grid_dependency_wait();   // for the maxima
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int chunk = threadIdx.x & 7, group = threadIdx.x >> 3;   // 8 columns, 4 rows
-  const int64_t c = c0 + chunk * 8;
-  const bool vec = ((reinterpret_cast<uintptr_t>(M) | (uintptr_t)(ld * (int64_t)sizeof(T))) & 15u) == 0;
-  auto load_slab = [&](int64_t s, Chunk<T> (&k)[4]) {
-    const int64_t r0 = s * kSlab + group * 4;
-    const T* at = M + r0 * ld;
-    if (r0 + 4 <= rows) {
+  const int word = warp * 4 + (lane & 3);
+  const int64_t c = c0 + word * PER_WORD;
+  LineScale ls[PER_WORD];
 #pragma unroll
-      for (int i = 0; i < 4; ++i, at += ld) k[i] = load_chunk(at, c, cols, vec);
-    } else {   // the last row again does not change a maximum, and its codes are not written
-#pragma unroll
-      for (int i = 0; i < 4; ++i) k[i] = load_chunk(M + min(r0 + i, rows - 1) * ld, c, cols, vec);
-    }
-  };
-
-  // Maxima of the strip's columns over all rows, in shared memory of every block.
-  auto column_tops = [&](bool finite_only, int slot) {
-    uint32_t top[8] = {};
-    if (sizeof(T) == 2 && !finite_only) {
-      uint32_t two[4] = {};
-      for (int64_t s = first; s < last; ++s) {
-        Chunk<T> k[4];
-        load_slab(s, k);
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-#pragma unroll
-          for (int j = 0; j < 4; ++j) two[j] = __vmaxu2(two[j], k[i].w[j] & 0x7FFF7FFFu);
-      }
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        top[2 * j] = two[j] << 16;
-        top[2 * j + 1] = two[j] & 0xFFFF0000u;
-      }
-    } else {
-      for (int64_t s = first; s < last; ++s) {
-        Chunk<T> k[4];
-        load_slab(s, k);
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-#pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            const uint32_t b = __float_as_uint(k[i].get(j)) & 0x7FFFFFFFu;
-            if (!finite_only || b < kInf) top[j] = max(top[j], b);
-          }
-      }
-    }
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      top[j] = max(top[j], __shfl_xor_sync(0xffffffffu, top[j], 8));
-      top[j] = max(top[j], __shfl_xor_sync(0xffffffffu, top[j], 16));
-      if (lane < 8) part[warp][chunk * 8 + j] = top[j];
-    }
-    __syncthreads();
-    if (threadIdx.x < kStrip) {
-      uint32_t m = 0;
-#pragma unroll
-      for (int w = 0; w < kThreads / 32; ++w) m = max(m, part[w][threadIdx.x]);
-      tops[slot][threadIdx.x] = m;
-    }
-    tc::cluster_sync();
-    uint32_t m = 0;
-    if (threadIdx.x < kStrip) {
-      const uint32_t at = tc::smem_addr(&tops[slot][threadIdx.x]);
-      for (int s = 0; s < shares; ++s) m = max(m, tc::load_cluster_u32(tc::cluster_addr_u32(at, (uint32_t)s)));
-    }
-    return m;   // of column c0 + threadIdx.x, in the first 64 threads
-  };
-
-  uint32_t top = column_tops(false, 0);
-  const bool bad = threadIdx.x < kStrip && top >= kInf;
-  if (__syncthreads_or(bad)) {                 // the same in all blocks of the cluster
-    const uint32_t fine = column_tops(true, 1);
-    if (bad) top = fine;
+  for (int e = 0; e < PER_WORD; ++e) {
+    ls[e] = c + e < cols ? line_scale(tops[c + e], marks[c + e] != 0) : line_scale(0u, false);
+    if (tile == 0 && lane < 4 && c + e < cols) scales[c + e] = scale_of(ls[e]);
   }
-  if (threadIdx.x < kStrip) {
-    const LineScale s = line_scale(top, bad);
-    line[threadIdx.x] = s;
-    if (share == 0 && c0 + threadIdx.x < cols) {
-      scales[c0 + threadIdx.x] = scale_of(s);
-      if (bad) raise_status(status, METIS_DEV_NONFINITE);
-    }
-  }
-  tc::cluster_arrive();                        // this block has read the others' maxima
+  copy_async_wait_all();
   __syncthreads();
-  LineScale ls[8];
+#pragma unroll 1
+  for (int piece = lane >> 2; piece < kTileRows / kPiece; piece += 8) {
+    const int left = n - piece * kPiece;
+    if (left <= 0) break;
+    const uint32_t* w = reinterpret_cast<const uint32_t*>(data + piece * kPieceBytes) + word;
+    uint32_t out[PER_WORD][4];
 #pragma unroll
-  for (int j = 0; j < 8; ++j) ls[j] = line[chunk * 8 + j];
-
-  int buf = 0;
-  for (int64_t s = first; s < last; ++s, buf ^= 1) {
-    const int64_t r0 = s * kSlab;
-    Chunk<T> k[4];
-    load_slab(s, k);
+    for (int i = 0; i < 4; ++i) {
+      uint32_t x[4];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      uint32_t b[4];
-      bool near = ls[j].a < 0.0f;
+      for (int j = 0; j < 4; ++j) x[j] = w[(4 * i + j) * (kRowBytes / 4)];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) b[i] = code_bits<T>(k[i].get(j), ls[j], near);
-      uint32_t w = pack4(b[0], b[1], b[2], b[3]);
-      if (near) w = four_codes_exact(k[0].get(j), k[1].get(j), k[2].get(j), k[3].get(j), fabsf(ls[j].a), ls[j].inv);
-      tile[buf][chunk * 8 + j][group] = w;
+      for (int e = 0; e < PER_WORD; ++e) {
+        float f[4];
+        uint32_t q[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) f[j] = __uint_as_float(sizeof(T) == 4 ? x[j] : e ? x[j] & 0xFFFF0000u : x[j] << 16);
+        if (ls[e].a < 0.0f) {
+          out[e][i] = four_codes_exact(f[0], f[1], f[2], f[3], -ls[e].a, ls[e].inv);
+          continue;
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) q[j] = code_bits<T>(f[j], ls[e]);
+        out[e][i] = pack4(q[0], q[1], q[2], q[3]);
+      }
     }
-    __syncthreads();   // the other buffer was read before the block came here
-    // 16 rows (16 bytes) of a column per thread and step
 #pragma unroll
-    for (int u = threadIdx.x; u < kStrip * 8; u += kThreads) {
-      const int64_t cc = c0 + (u >> 3), rr = r0 + (u & 7) * 16;
-      if (cc >= cols || rr >= rows) continue;
-      const uint32_t* from = &tile[buf][u >> 3][(u & 7) * 4];
-      int8_t* dst = codes + cc * ldq + rr;
-      if (rr + 16 <= rows) {
-        *reinterpret_cast<uint4*>(dst) = make_uint4(from[0], from[1], from[2], from[3]);
+    for (int e = 0; e < PER_WORD; ++e) {
+      if (c + e >= cols) continue;
+      int8_t* dst = codes + (c + e) * ldq + r0 + piece * kPiece;
+      if (left >= kPiece) {
+        *reinterpret_cast<uint4*>(dst) = make_uint4(out[e][0], out[e][1], out[e][2], out[e][3]);
       } else {
-        for (int i = 0; rr + i < rows; ++i) dst[i] = (int8_t)(from[i >> 2] >> (8 * (i & 3)));
+#pragma unroll
+        for (int i = 0; i < kPiece; ++i)
+          if (i < left) dst[i] = (int8_t)(out[e][i >> 2] >> (8 * (i & 3)));
       }
     }
   }
-  tc::cluster_wait();                          // nor does a block leave while its own are read
-  tc::grid_dependency_wait();                  // the row kernel before this one, beside which it ran
 }
 
-template <typename T, int GROUP, bool HELD>
-cudaError_t launch_rows(const T* M, int64_t rows, int64_t cols, int64_t ld, const metis_int8* q, uint32_t* status,
-                        cudaStream_t st) {
-  constexpr int BLOCK = GROUP > kThreads ? GROUP : kThreads;
-  const int64_t blocks = (rows + BLOCK / GROUP - 1) / (BLOCK / GROUP);
-  quantize_i8_rows_kernel<T, GROUP, HELD><<<(unsigned)blocks, BLOCK, 0, st>>>(M, rows, cols, ld, q->codes, q->ld, q->scales, status);
+// ---------------------------------------------------------------- launches
+template <typename T, int GROUP, bool TOPS>
+cudaError_t launch_rows(const T* M, int64_t rows, int64_t cols, int64_t ld, const metis_int8* q, uint32_t* tops,
+                        uint32_t* marks, uint32_t* status, int sm_count, cudaStream_t st) {
+  constexpr int BLOCK = GROUP == 32 ? kThreads : GROUP;
+  const int64_t blocks = std::min<int64_t>((rows + BLOCK / GROUP - 1) / (BLOCK / GROUP),
+                                           (int64_t)sm_count * std::max(1, kRowThreads<T, TOPS> / BLOCK));
+  quantize_i8_rows_kernel<T, GROUP, TOPS><<<(unsigned)blocks, BLOCK, 0, st>>>(
+      M, rows, (int)cols, ld, q ? q->codes : nullptr, q ? q->ld : 0, q ? q->scales : nullptr, tops, marks, status);
   count_launch();
   return cudaGetLastError();
 }
 
 // The smallest group that holds a row; where rows are too few to fill the SMs, the largest that
-// has a chunk for each thread.
-template <typename T>
-cudaError_t run_rows(const T* M, int64_t rows, int64_t cols, int64_t ld, const metis_int8* q, uint32_t* status, int sm_count,
-                     cudaStream_t st) {
+// has a chunk or two for each thread.
+template <typename T, bool TOPS>
+cudaError_t run_rows(const T* M, int64_t rows, int64_t cols, int64_t ld, const metis_int8* q, uint32_t* tops,
+                     uint32_t* marks, uint32_t* status, int sm_count, cudaStream_t st) {
   const int64_t chunks = (cols + 7) / 8;
-  if (chunks > 512 * kHeld) return launch_rows<T, 512, false>(M, rows, cols, ld, q, status, st);
-  const bool few = rows < 4 * (int64_t)sm_count;
-  if (few ? chunks <= 64 : chunks <= 32 * kHeld) return launch_rows<T, 32, true>(M, rows, cols, ld, q, status, st);
-  if (few ? chunks <= 256 : chunks <= 128 * kHeld) return launch_rows<T, 128, true>(M, rows, cols, ld, q, status, st);
-  return launch_rows<T, 512, true>(M, rows, cols, ld, q, status, st);
+  const int64_t need = rows < 4 * (int64_t)sm_count ? std::min<int64_t>(512, chunks / 2) : 0;
+  const int64_t threads = std::max(need, (chunks + kHeld - 1) / kHeld);
+  if (threads <= 32) return launch_rows<T, 32, TOPS>(M, rows, cols, ld, q, tops, marks, status, sm_count, st);
+  if (threads <= 64) return launch_rows<T, 64, TOPS>(M, rows, cols, ld, q, tops, marks, status, sm_count, st);
+  if (threads <= 128) return launch_rows<T, 128, TOPS>(M, rows, cols, ld, q, tops, marks, status, sm_count, st);
+  if (threads <= 256) return launch_rows<T, 256, TOPS>(M, rows, cols, ld, q, tops, marks, status, sm_count, st);
+  return launch_rows<T, 512, TOPS>(M, rows, cols, ld, q, tops, marks, status, sm_count, st);
 }
 
-// beside: the launch before this one on the stream is the row kernel of the same matrix (an
-// ordinary launch); the two run side by side.
-template <typename T>
-cudaError_t run_cols(const T* M, int64_t rows, int64_t cols, int64_t ld, const metis_int8* q, uint32_t* status, bool beside,
-                     cudaStream_t st) {
-  const int64_t slabs = (rows + kSlab - 1) / kSlab;
-  const int shares = (int)std::min<int64_t>(8, slabs);
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3((unsigned)((cols + kStrip - 1) / kStrip * shares));
-  cfg.blockDim = dim3(kThreads);
-  cfg.stream = st;
-  cudaLaunchAttribute attr[2];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = (unsigned)shares;
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = 1;
-  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[1].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = beside ? 2 : 1;
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, quantize_i8_cols_kernel<T>, M, rows, cols, ld, q->codes, q->ld, q->scales, status);
-  if (e == cudaSuccess) count_launch();
-  return e;
-}
+constexpr int64_t kMostHeld = 512 * kHeld * 8;   // columns
 
 template <typename T>
 cudaError_t run_quantize(const T* M, int64_t rows, int64_t cols, int64_t ld, const metis_int8* row, const metis_int8* col,
                          uint32_t* status, int sm_count, cudaStream_t st) {
-  if (row) {
-    const cudaError_t e = run_rows(M, rows, cols, ld, row, status, sm_count, st);
-    if (e != cudaSuccess || !col) return e;
+  uint32_t *tops = nullptr, *marks = nullptr;
+  cudaError_t e = cudaSuccess;
+  if (col) {
+    tops = col->scratch;
+    marks = col->scratch + cols;
+    if ((e = cudaMemsetAsync(tops, 0, (size_t)cols * 8, st)) != cudaSuccess) return e;
   }
-  return run_cols(M, rows, cols, ld, col, status, row != nullptr, st);
+  if (row && cols > kMostHeld) {
+    quantize_i8_long_rows_kernel<T><<<(unsigned)rows, 512, 0, st>>>(M, (int)cols, ld, row->codes, row->ld, row->scales, status);
+    count_launch();
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  }
+  if (!col) return cols > kMostHeld ? e : run_rows<T, false>(M, rows, cols, ld, row, nullptr, nullptr, status, sm_count, st);
+  if (row && cols <= kMostHeld) {
+    e = run_rows<T, true>(M, rows, cols, ld, row, tops, marks, status, sm_count, st);
+  } else {   // only the maxima: columns in spans
+    for (int64_t c = 0; c < cols && e == cudaSuccess; c += kMostHeld)
+      e = run_rows<T, true>(M + c, rows, std::min(kMostHeld, cols - c), ld, nullptr, tops + c, marks + c, status, sm_count, st);
+  }
+  if (e != cudaSuccess) return e;
+  constexpr int COLS = kRowBytes / (int)sizeof(T);
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3((unsigned)((cols + COLS - 1) / COLS * ((rows + kTileRows - 1) / kTileRows)));
+  cfg.blockDim = dim3(kThreads);
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  e = cudaLaunchKernelEx(&cfg, quantize_i8_cols_kernel<T>, M, rows, cols, ld, col->codes, col->ld, col->scales,
+                         (const uint32_t*)tops, (const uint32_t*)marks);
+  if (e == cudaSuccess) count_launch();
+  return e;
 }
 
 }  // namespace
