@@ -339,9 +339,11 @@ metis_status metis_lora_realign(metis_ctx* ctx, float* W_res, int64_t m, int64_t
  * the product that reads it.  codes 16-byte aligned, ld >= inner and a multiple of 16;
  * the bytes from inner to ld of a line are neither read nor written.  Unlike the NVFP4
  * operands these have no limits on outer and inner besides 1 <= outer, inner < 2^31.
- * scratch: 2 * outer words that a column-wise quantization into this tensor overwrites (it
- * gathers the maxima there); may be NULL in every other use.
+ * scratch: METIS_INT8_SCRATCH * outer words that a column-wise quantization into this tensor
+ * overwrites (it gathers the maxima there); may be NULL in every other use.
  */
+#define METIS_INT8_SCRATCH_COPIES 8
+#define METIS_INT8_SCRATCH (METIS_INT8_SCRATCH_COPIES + 1)
 typedef struct {
   int8_t* codes;
   float* scales;

@@ -36,6 +36,7 @@ STATUS_NAMES = {0: "OK", 1: "ERR_ARG", 2: "ERR_SHAPE", 3: "ERR_ALIGN", 4: "ERR_A
                 6: "ERR_WORKSPACE"}
 DEV_NUMERIC, DEV_NONFINITE, DEV_TIMEOUT = 1, 2, 4
 OUT_F32, OUT_BF16 = 0, 1
+INT8_SCRATCH = 9    # METIS_INT8_SCRATCH
 _DTYPES = {torch.float32: OUT_F32, torch.bfloat16: OUT_BF16}
 
 EXPORTED = ["metis_create", "metis_destroy", "metis_set_stream", "metis_status_str", "metis_last_error",
@@ -235,7 +236,7 @@ class Int8:
 
     def with_scratch(self):
         if self.scratch is None:
-            self.scratch = torch.empty(2 * self.outer, dtype=torch.int32, device=self.codes.device)
+            self.scratch = torch.empty(INT8_SCRATCH * self.outer, dtype=torch.int32, device=self.codes.device)
             self.struct.scratch = self.scratch.data_ptr()
         return self
 

@@ -628,7 +628,7 @@ metis_status check_quantize_int8(metis_ctx* ctx, const void* M, int64_t rows, in
   if (rowwise && (s = check_int8(ctx, rowwise, "rowwise")) != METIS_OK) return s;
   if (colwise && (s = check_int8(ctx, colwise, "colwise")) != METIS_OK) return s;
   if (colwise && (!colwise->scratch || (reinterpret_cast<uintptr_t>(colwise->scratch) & 3u)))
-    return fail(ctx, colwise->scratch ? METIS_ERR_ALIGN : METIS_ERR_ARG, "colwise: needs an aligned scratch of 2 * outer words");
+    return fail(ctx, colwise->scratch ? METIS_ERR_ALIGN : METIS_ERR_ARG, "colwise: needs an aligned scratch of METIS_INT8_SCRATCH * outer words");
   if (rowwise && (rowwise->outer != rows || rowwise->inner != cols))
     return fail(ctx, METIS_ERR_SHAPE, "rowwise: expected outer x inner = rows x cols");
   if (colwise && (colwise->outer != cols || colwise->inner != rows))

@@ -68,21 +68,25 @@ __device__ __noinline__ int code_exact(float x, float a, float inv) {
   return x < 0.0f ? -c : c;
 }
 
-// The code in the low byte, for a line that needs no fp64 comparison.
+// The code in the low byte, for a line that needs no fp64 comparison; fp32: near a border it is
+// open and `near` is raised.
 template <typename T>
-__device__ __forceinline__ uint32_t code_bits(float x, const LineScale& s) {
+__device__ __forceinline__ uint32_t code_bits(float x, const LineScale& s, bool& near) {
   const float y = __fmaf_rn(x, s.inv, __fmul_rn(x, s.lo));
-  float t = __fadd_rn(y, 12582912.0f);
-  if constexpr (sizeof(T) == 4) {
-    if (fabsf(__fsub_rn(y, __fsub_rn(t, 12582912.0f))) > 0.49996f) {
-      const float m = fabsf(x), n = floorf(fabsf(y)), odd = 2.0f * n + 1.0f;
-      const float l = __fmul_rn(254.0f, m), r = __fmul_rn(odd, s.a);
-      const float d = __fadd_rn(__fsub_rn(l, r), __fsub_rn(__fmaf_rn(254.0f, m, -l), __fmaf_rn(odd, s.a, -r)));
-      const float c = n + (d > 0.0f || (d == 0.0f && ((int)n & 1)) ? 1.0f : 0.0f);
-      t = __fadd_rn(copysignf(c, x), 12582912.0f);
-    }
-  }
+  const float t = __fadd_rn(y, 12582912.0f);
+  if constexpr (sizeof(T) == 4) near |= fabsf(__fsub_rn(y, __fsub_rn(t, 12582912.0f))) > 0.49996f;
   return __float_as_uint(t);
+}
+// The same with the comparison.
+__device__ __forceinline__ uint32_t code_at_border(float x, const LineScale& s) {
+  const float y = __fmaf_rn(x, s.inv, __fmul_rn(x, s.lo));
+  const float t = __fadd_rn(y, 12582912.0f);
+  if (!(fabsf(__fsub_rn(y, __fsub_rn(t, 12582912.0f))) > 0.49996f)) return __float_as_uint(t);
+  const float m = fabsf(x), n = floorf(fabsf(y)), odd = 2.0f * n + 1.0f;
+  const float l = __fmul_rn(254.0f, m), r = __fmul_rn(odd, s.a);
+  const float d = __fadd_rn(__fsub_rn(l, r), __fsub_rn(__fmaf_rn(254.0f, m, -l), __fmaf_rn(odd, s.a, -r)));
+  const float c = n + (d > 0.0f || (d == 0.0f && ((int)n & 1)) ? 1.0f : 0.0f);
+  return __float_as_uint(__fadd_rn(copysignf(c, x), 12582912.0f));
 }
 
 __device__ __forceinline__ uint32_t pack4(uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
@@ -147,24 +151,26 @@ __device__ __forceinline__ uint32_t chunk_finite_top(const Chunk<T>& k, uint32_t
 }
 
 // The eight codes of a chunk under one scale, packed.
-template <typename T>
-__device__ __noinline__ uint2 chunk_codes_exact(Chunk<T> k, float a, float inv) {
-  uint32_t b[8];
-#pragma unroll
-  for (int i = 0; i < 8; ++i) b[i] = (uint32_t)code_exact(k.get(i), a, inv);
-  return make_uint2(pack4(b[0], b[1], b[2], b[3]), pack4(b[4], b[5], b[6], b[7]));
+// Four at a time where something is open: code_at_border, or code_exact for a line with s.a < 0.
+__device__ __noinline__ uint32_t four_open(float x0, float x1, float x2, float x3, float a, float inv, float lo) {
+  const LineScale s{a, inv, lo};
+  if (a < 0.0f)
+    return pack4((uint32_t)code_exact(x0, -a, inv), (uint32_t)code_exact(x1, -a, inv), (uint32_t)code_exact(x2, -a, inv),
+                 (uint32_t)code_exact(x3, -a, inv));
+  return pack4(code_at_border(x0, s), code_at_border(x1, s), code_at_border(x2, s), code_at_border(x3, s));
 }
-__device__ __noinline__ uint32_t four_codes_exact(float x0, float x1, float x2, float x3, float a, float inv) {
-  return pack4((uint32_t)code_exact(x0, a, inv), (uint32_t)code_exact(x1, a, inv), (uint32_t)code_exact(x2, a, inv),
-               (uint32_t)code_exact(x3, a, inv));
+template <typename T>
+__device__ __forceinline__ uint32_t four_codes(float x0, float x1, float x2, float x3, const LineScale& s) {
+  bool near = s.a < 0.0f;
+  const uint32_t b0 = code_bits<T>(x0, s, near), b1 = code_bits<T>(x1, s, near), b2 = code_bits<T>(x2, s, near),
+                 b3 = code_bits<T>(x3, s, near);
+  if (near) return four_open(x0, x1, x2, x3, s.a, s.inv, s.lo);
+  return pack4(b0, b1, b2, b3);
 }
 template <typename T>
 __device__ __forceinline__ uint2 chunk_codes(const Chunk<T>& k, const LineScale& s) {
-  if (s.a < 0.0f) return chunk_codes_exact(k, -s.a, s.inv);
-  uint32_t b[8];
-#pragma unroll
-  for (int i = 0; i < 8; ++i) b[i] = code_bits<T>(k.get(i), s);
-  return make_uint2(pack4(b[0], b[1], b[2], b[3]), pack4(b[4], b[5], b[6], b[7]));
+  return make_uint2(four_codes<T>(k.get(0), k.get(1), k.get(2), k.get(3), s),
+                    four_codes<T>(k.get(4), k.get(5), k.get(6), k.get(7), s));
 }
 
 // Eight codes; the bytes of columns >= cols are not written.
@@ -183,28 +189,24 @@ __device__ __forceinline__ void store_codes(int8_t* row, int c, int cols, uint2 
 // and the codes, so it is read once; the next row is loaded before the work on one begins
 // (without that a block waited for its loads most of the time: 21 us at 8192 x 4096 bf16, 19 with
 // it).  A block is one group, or eight where a group is a warp, and goes on to further rows.
-//   TOPS: a thread meets the same columns in every row, and gathers their maxima on the way;
-// they are joined in `tops` by integer atomicMax (the order does not matter), a warp's 32
-// neighbours at a time.  codes == nullptr: only that.
-constexpr int kHeld = 4;
+//   TOPS: a thread meets the same columns in every row; it keeps their maxima in shared memory
+// (its own words, 64 registers a thread are full), and the block joins them into one of kCopies
+// copies of `tops` by integer atomicMax, whose order does not matter.  Many copies and few blocks,
+// since blocks that meet at an address wait for one another (888 blocks and one copy took 10 us
+// longer than the rows alone).  codes == nullptr: only that.
+constexpr int kCopies = METIS_INT8_SCRATCH_COPIES;
 
-// Column maxima of a thread's chunks: bf16 two to a word (their bits order like the values).
+// Larger of the magnitudes in `top` and in a word of a chunk (bf16 two to a word; their bits order
+// like the values).
 template <typename T>
-struct ColumnTops {
-  static constexpr int WORDS = 2 * (int)sizeof(T);
-  uint32_t w[kHeld][WORDS];
-  __device__ __forceinline__ void add(int i, const Chunk<T>& k) {
-#pragma unroll
-    for (int j = 0; j < WORDS; ++j) {
-      if constexpr (sizeof(T) == 2) w[i][j] = __vmaxu2(w[i][j], k.w[j] & 0x7FFF7FFFu);
-      else w[i][j] = max(w[i][j], k.w[j] & 0x7FFFFFFFu);
-    }
-  }
-  __device__ __forceinline__ uint32_t get(int i, int j) const {   // fp32 bits
-    if constexpr (sizeof(T) == 4) return w[i][j];
-    else return (j & 1) ? w[i][j >> 1] & 0xFFFF0000u : w[i][j >> 1] << 16;
-  }
-};
+__device__ __forceinline__ uint32_t word_top(uint32_t top, uint32_t w) {
+  if constexpr (sizeof(T) == 2) return __vmaxu2(top, w & 0x7FFF7FFFu);
+  else return max(top, w & 0x7FFFFFFFu);
+}
+template <int GROUP>
+__device__ __forceinline__ void group_sync(int group) {
+  asm volatile("bar.sync %0, %1;" ::"r"(group + 1), "n"(GROUP) : "memory");
+}
 
 // A chunk with entries that are not finite: they are left out and their columns marked.
 template <typename T>
@@ -220,57 +222,74 @@ __device__ __noinline__ Chunk<T> mark_nonfinite(Chunk<T> k, int c, uint32_t* mar
   return k;
 }
 
-// Threads of an SM: what the registers allow.
-template <typename T, bool TOPS>
-constexpr int kRowThreads = (sizeof(T) == 2 ? 1024 : 640) - (TOPS ? (sizeof(T) == 2 ? 256 : 128) : 0);
+// Threads of a block (several groups) and blocks of an SM: what the registers allow.
+template <int GROUP, bool TOPS>
+constexpr int kRowBlock = TOPS ? 512 : GROUP == 32 ? kThreads : GROUP;
+template <typename T, int GROUP, int HELD, bool TOPS>
+constexpr int kRowBlocks = (HELD * (int)sizeof(T) == 16 ? 640 : 1024) / kRowBlock<GROUP, TOPS>;
 
-template <typename T, int GROUP, bool TOPS>
-__global__ void __launch_bounds__(GROUP == 32 ? kThreads : GROUP, kRowThreads<T, TOPS> / (GROUP == 32 ? kThreads : GROUP))
+template <typename T, int GROUP, int HELD, bool TOPS>
+__global__ void __launch_bounds__(kRowBlock<GROUP, TOPS>, kRowBlocks<T, GROUP, HELD, TOPS>)
     quantize_i8_rows_kernel(const T* __restrict__ M, int64_t rows, int cols, int64_t ld, int8_t* __restrict__ codes,
-                            int64_t ldq, float* __restrict__ scales, uint32_t* __restrict__ tops,
+                            int64_t ldq, float* __restrict__ scales, uint32_t* __restrict__ tops, int64_t tops_pitch,
                             uint32_t* __restrict__ marks, uint32_t* status) {
-  constexpr int BLOCK = GROUP == 32 ? kThreads : GROUP;
+  constexpr int BLOCK = kRowBlock<GROUP, TOPS>, GROUPS = BLOCK / GROUP, VECS = (int)sizeof(T) / 2;
   __shared__ uint32_t part[2][2][BLOCK / 32];
+  extern __shared__ __align__(16) uint4 col[];   // [HELD][VECS][BLOCK]
   tc::grid_launch_dependents();   // what follows may start loading
-  const int t = threadIdx.x % GROUP;
-  const int64_t step = (int64_t)gridDim.x * (BLOCK / GROUP);
-  int64_t r = (int64_t)blockIdx.x * (BLOCK / GROUP) + threadIdx.x / GROUP;
+  const int t = threadIdx.x % GROUP, group = threadIdx.x / GROUP;
+  const int64_t step = (int64_t)gridDim.x * GROUPS;
+  int64_t r = (int64_t)blockIdx.x * GROUPS + group;
 
-  auto load_row = [&](int64_t r, Chunk<T> (&k)[kHeld]) {
+  auto load_row = [&](int64_t r, Chunk<T> (&k)[HELD]) {
     const T* row = M + r * ld;
     const bool vec = (reinterpret_cast<uintptr_t>(row) & 15u) == 0;
 #pragma unroll
-    for (int i = 0; i < kHeld; ++i) k[i] = load_chunk(row, (i * GROUP + t) * 8, cols, vec);
+    for (int i = 0; i < HELD; ++i) k[i] = load_chunk(row, (i * GROUP + t) * 8, cols, vec);
   };
   auto over_row = [&](uint32_t top, uint32_t* slot) {
     top = __reduce_max_sync(0xffffffffu, top);
     if constexpr (GROUP > 32) {
       if ((threadIdx.x & 31) == 0) slot[threadIdx.x >> 5] = top;
-      __syncthreads();
+      if constexpr (GROUPS == 1) __syncthreads();
+      else group_sync<GROUP>(group);
 #pragma unroll
-      for (int i = 0; i < GROUP / 32; ++i) top = max(top, slot[i]);
+      for (int i = 0; i < GROUP / 32; ++i) top = max(top, slot[group * (GROUP / 32) + i]);
     }
     return top;
   };
+  auto add_to_columns = [&](int i, const Chunk<T>& k) {
+#pragma unroll
+    for (int v = 0; v < VECS; ++v) {
+      uint4& at = col[(i * VECS + v) * BLOCK + threadIdx.x];
+      uint4 m = at;
+      m.x = word_top<T>(m.x, k.w[4 * v]);
+      m.y = word_top<T>(m.y, k.w[4 * v + 1]);
+      m.z = word_top<T>(m.z, k.w[4 * v + 2]);
+      m.w = word_top<T>(m.w, k.w[4 * v + 3]);
+      at = m;
+    }
+  };
 
-  ColumnTops<T> col{};
-  Chunk<T> next[kHeld];
+  if constexpr (TOPS)
+    for (int i = 0; i < HELD * VECS; ++i) col[i * BLOCK + threadIdx.x] = make_uint4(0, 0, 0, 0);
+  Chunk<T> next[HELD];
   if (r < rows) load_row(r, next);
   for (int turn = 0; r < rows; r += step, turn ^= 1) {
-    Chunk<T> held[kHeld];
+    Chunk<T> held[HELD];
 #pragma unroll
-    for (int i = 0; i < kHeld; ++i) held[i] = next[i];
+    for (int i = 0; i < HELD; ++i) held[i] = next[i];
     if (r + step < rows) load_row(r + step, next);
     uint32_t top = 0;
 #pragma unroll
-    for (int i = 0; i < kHeld; ++i) top = chunk_top(held[i], top);
+    for (int i = 0; i < HELD; ++i) top = chunk_top(held[i], top);
     if constexpr (TOPS) {
       if (top < kInf) {
 #pragma unroll
-        for (int i = 0; i < kHeld; ++i) col.add(i, held[i]);
+        for (int i = 0; i < HELD; ++i) add_to_columns(i, held[i]);
       } else {
 #pragma unroll
-        for (int i = 0; i < kHeld; ++i) col.add(i, mark_nonfinite(held[i], (i * GROUP + t) * 8, marks, status));
+        for (int i = 0; i < HELD; ++i) add_to_columns(i, mark_nonfinite(held[i], (i * GROUP + t) * 8, marks, status));
       }
       if (!codes) continue;
     }
@@ -279,7 +298,7 @@ __global__ void __launch_bounds__(GROUP == 32 ? kThreads : GROUP, kRowThreads<T,
     if (bad) {
       top = 0;
 #pragma unroll
-      for (int i = 0; i < kHeld; ++i) top = chunk_finite_top(held[i], top);
+      for (int i = 0; i < HELD; ++i) top = chunk_finite_top(held[i], top);
       top = over_row(top, part[turn][1]);
     }
     const LineScale s = line_scale(top, bad);
@@ -289,28 +308,23 @@ __global__ void __launch_bounds__(GROUP == 32 ? kThreads : GROUP, kRowThreads<T,
     }
     int8_t* out = codes + r * ldq;
 #pragma unroll
-    for (int i = 0; i < kHeld; ++i) {
+    for (int i = 0; i < HELD; ++i) {
       const int c = (i * GROUP + t) * 8;
       if (c < cols) store_codes(out, c, cols, chunk_codes(held[i], s));
     }
   }
   if constexpr (TOPS) {
-    // lane l holds columns 8 l .. 8 l + 7 of 256; turned through shared memory, 32 neighbours at a time
-    __shared__ uint32_t turned[BLOCK / 32][32 * 9];
-    uint32_t* mine = turned[threadIdx.x >> 5];
-    const int lane = threadIdx.x & 31, warp_t = t & ~31;
+    __syncthreads();
+    uint32_t* const copy = tops + (int64_t)(blockIdx.x % kCopies) * tops_pitch;
+    constexpr int PER_WORD = 4 / (int)sizeof(T);
+    for (int c = threadIdx.x; c < cols; c += BLOCK) {
+      const int chunk = c >> 3, i = chunk / GROUP, word = (c & 7) / PER_WORD;   // word of the chunk
+      const uint32_t* at = reinterpret_cast<const uint32_t*>(col + (i * VECS + word / 4) * BLOCK + chunk % GROUP) + (word & 3);
+      uint32_t m = 0;
 #pragma unroll
-    for (int i = 0; i < kHeld; ++i) {
-#pragma unroll
-      for (int j = 0; j < 8; ++j) mine[lane * 9 + j] = col.get(i, j);
-      __syncwarp();
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const int e = j * 32 + lane, c = (i * GROUP + warp_t) * 8 + e;
-        const uint32_t m = mine[(e >> 3) * 9 + (e & 7)];
-        if (c < cols && m) atomicMax(&tops[c], m);
-      }
-      __syncwarp();
+      for (int g = 0; g < GROUPS; ++g) m = word_top<T>(m, at[g * GROUP * 4]);
+      if constexpr (sizeof(T) == 2) m = (c & 1) ? m & 0xFFFF0000u : m << 16;
+      if (m) atomicMax(&copy[c], m);
     }
   }
 }
@@ -399,7 +413,11 @@ __global__ void __launch_bounds__(kThreads, 5) quantize_i8_cols_kernel(const T* 
   LineScale ls[PER_WORD];
 #pragma unroll
   for (int e = 0; e < PER_WORD; ++e) {
-    ls[e] = c + e < cols ? line_scale(tops[c + e], marks[c + e] != 0) : line_scale(0u, false);
+    uint32_t top = 0;
+    if (c + e < cols)
+#pragma unroll
+      for (int i = 0; i < kCopies; ++i) top = max(top, tops[i * cols + c + e]);
+    ls[e] = line_scale(top, c + e < cols && marks[c + e] != 0);
     if (tile == 0 && lane < 4 && c + e < cols) scales[c + e] = scale_of(ls[e]);
   }
   copy_async_wait_all();
@@ -418,16 +436,9 @@ __global__ void __launch_bounds__(kThreads, 5) quantize_i8_cols_kernel(const T* 
 #pragma unroll
       for (int e = 0; e < PER_WORD; ++e) {
         float f[4];
-        uint32_t q[4];
 #pragma unroll
         for (int j = 0; j < 4; ++j) f[j] = __uint_as_float(sizeof(T) == 4 ? x[j] : e ? x[j] & 0xFFFF0000u : x[j] << 16);
-        if (ls[e].a < 0.0f) {
-          out[e][i] = four_codes_exact(f[0], f[1], f[2], f[3], -ls[e].a, ls[e].inv);
-          continue;
-        }
-#pragma unroll
-        for (int j = 0; j < 4; ++j) q[j] = code_bits<T>(f[j], ls[e]);
-        out[e][i] = pack4(q[0], q[1], q[2], q[3]);
+        out[e][i] = four_codes<T>(f[0], f[1], f[2], f[3], ls[e]);
       }
     }
 #pragma unroll
@@ -446,34 +457,44 @@ __global__ void __launch_bounds__(kThreads, 5) quantize_i8_cols_kernel(const T* 
 }
 
 // ---------------------------------------------------------------- launches
-template <typename T, int GROUP, bool TOPS>
+template <typename T, int GROUP, int HELD, bool TOPS>
 cudaError_t launch_rows(const T* M, int64_t rows, int64_t cols, int64_t ld, const metis_int8* q, uint32_t* tops,
-                        uint32_t* marks, uint32_t* status, int sm_count, cudaStream_t st) {
-  constexpr int BLOCK = GROUP == 32 ? kThreads : GROUP;
-  const int64_t blocks = std::min<int64_t>((rows + BLOCK / GROUP - 1) / (BLOCK / GROUP),
-                                           (int64_t)sm_count * std::max(1, kRowThreads<T, TOPS> / BLOCK));
-  quantize_i8_rows_kernel<T, GROUP, TOPS><<<(unsigned)blocks, BLOCK, 0, st>>>(
-      M, rows, (int)cols, ld, q ? q->codes : nullptr, q ? q->ld : 0, q ? q->scales : nullptr, tops, marks, status);
+                        int64_t pitch, uint32_t* marks, uint32_t* status, int sm_count, cudaStream_t st) {
+  constexpr int BLOCK = kRowBlock<GROUP, TOPS>, GROUPS = BLOCK / GROUP;
+  constexpr int SMEM = TOPS ? HELD * (int)sizeof(T) / 2 * BLOCK * 16 : 0;
+  const int64_t blocks = std::min<int64_t>((rows + GROUPS - 1) / GROUPS, (int64_t)sm_count * kRowBlocks<T, GROUP, HELD, TOPS>);
+  auto kern = quantize_i8_rows_kernel<T, GROUP, HELD, TOPS>;
+  if (SMEM > 48 * 1024 - 1024) {
+    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM);
+    if (e != cudaSuccess) return e;
+  }
+  kern<<<(unsigned)blocks, BLOCK, SMEM, st>>>(M, rows, (int)cols, ld, q ? q->codes : nullptr, q ? q->ld : 0,
+                                              q ? q->scales : nullptr, tops, pitch, marks, status);
   count_launch();
   return cudaGetLastError();
 }
 
-// The smallest group that holds a row; where rows are too few to fill the SMs, the largest that
-// has a chunk or two for each thread.
+// A thread holds 64 bytes of a row, or 128 for the longest fp32 rows: the smallest group that
+// holds a row; where rows are too few to fill the SMs, the largest that has a chunk or two for
+// each thread.
 template <typename T, bool TOPS>
-cudaError_t run_rows(const T* M, int64_t rows, int64_t cols, int64_t ld, const metis_int8* q, uint32_t* tops,
+cudaError_t run_rows(const T* M, int64_t rows, int64_t cols, int64_t ld, const metis_int8* q, uint32_t* tops, int64_t pitch,
                      uint32_t* marks, uint32_t* status, int sm_count, cudaStream_t st) {
+  constexpr int HELD = 8 / (int)sizeof(T);
   const int64_t chunks = (cols + 7) / 8;
   const int64_t need = rows < 4 * (int64_t)sm_count ? std::min<int64_t>(512, chunks / 2) : 0;
-  const int64_t threads = std::max(need, (chunks + kHeld - 1) / kHeld);
-  if (threads <= 32) return launch_rows<T, 32, TOPS>(M, rows, cols, ld, q, tops, marks, status, sm_count, st);
-  if (threads <= 64) return launch_rows<T, 64, TOPS>(M, rows, cols, ld, q, tops, marks, status, sm_count, st);
-  if (threads <= 128) return launch_rows<T, 128, TOPS>(M, rows, cols, ld, q, tops, marks, status, sm_count, st);
-  if (threads <= 256) return launch_rows<T, 256, TOPS>(M, rows, cols, ld, q, tops, marks, status, sm_count, st);
-  return launch_rows<T, 512, TOPS>(M, rows, cols, ld, q, tops, marks, status, sm_count, st);
+  const int64_t threads = std::max(need, (chunks + HELD - 1) / HELD);
+#define METIS_ROWS(G, H) launch_rows<T, G, H, TOPS>(M, rows, cols, ld, q, tops, pitch, marks, status, sm_count, st)
+  if (threads <= 32) return METIS_ROWS(32, HELD);
+  if (threads <= 64) return METIS_ROWS(64, HELD);
+  if (threads <= 128) return METIS_ROWS(128, HELD);
+  if (threads <= 256) return METIS_ROWS(256, HELD);
+  if (threads <= 512) return METIS_ROWS(512, HELD);
+  return METIS_ROWS(512, 4);
+#undef METIS_ROWS
 }
 
-constexpr int64_t kMostHeld = 512 * kHeld * 8;   // columns
+constexpr int64_t kMostHeld = 512 * 4 * 8;   // columns
 
 template <typename T>
 cudaError_t run_quantize(const T* M, int64_t rows, int64_t cols, int64_t ld, const metis_int8* row, const metis_int8* col,
@@ -482,20 +503,20 @@ cudaError_t run_quantize(const T* M, int64_t rows, int64_t cols, int64_t ld, con
   cudaError_t e = cudaSuccess;
   if (col) {
     tops = col->scratch;
-    marks = col->scratch + cols;
-    if ((e = cudaMemsetAsync(tops, 0, (size_t)cols * 8, st)) != cudaSuccess) return e;
+    marks = col->scratch + kCopies * cols;
+    if ((e = cudaMemsetAsync(tops, 0, (size_t)cols * 4 * (kCopies + 1), st)) != cudaSuccess) return e;
   }
   if (row && cols > kMostHeld) {
     quantize_i8_long_rows_kernel<T><<<(unsigned)rows, 512, 0, st>>>(M, (int)cols, ld, row->codes, row->ld, row->scales, status);
     count_launch();
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
   }
-  if (!col) return cols > kMostHeld ? e : run_rows<T, false>(M, rows, cols, ld, row, nullptr, nullptr, status, sm_count, st);
+  if (!col) return cols > kMostHeld ? e : run_rows<T, false>(M, rows, cols, ld, row, nullptr, 0, nullptr, status, sm_count, st);
   if (row && cols <= kMostHeld) {
-    e = run_rows<T, true>(M, rows, cols, ld, row, tops, marks, status, sm_count, st);
+    e = run_rows<T, true>(M, rows, cols, ld, row, tops, cols, marks, status, sm_count, st);
   } else {   // only the maxima: columns in spans
     for (int64_t c = 0; c < cols && e == cudaSuccess; c += kMostHeld)
-      e = run_rows<T, true>(M + c, rows, std::min(kMostHeld, cols - c), ld, nullptr, tops + c, marks + c, status, sm_count, st);
+      e = run_rows<T, true>(M + c, rows, std::min(kMostHeld, cols - c), ld, nullptr, tops + c, cols, marks + c, status, sm_count, st);
   }
   if (e != cudaSuccess) return e;
   constexpr int COLS = kRowBytes / (int)sizeof(T);
