@@ -274,6 +274,7 @@ def _run_adamw(s):
     # the 8-bit states are returned as their whole numbers, codes and shared exponents: equal or not
     names = ("p", "m", "v", "me", "ve") if s["bits"] == 8 else ("p", "m", "v")
     if own:
+        _whole_spans(s)
         s["opt"].step()
         return {k: s[k] for k in names}
     s["step"] += 1
@@ -299,6 +300,21 @@ def _run_adamw(s):
         p = bits.view(torch.float32)
     s["p"] = p.to(_dtype(s["dtype"]))
     return {k: s[k] for k in names}
+
+
+def _whole_spans(s):
+    """The framework's calls step the same elements as the plain form: a tensor's whole span of the flat
+    buffers, the rest of its last BLOCK included, whose outputs are compared too."""
+    if "spans" in s:
+        return
+    group, at, s["spans"] = s["opt"].param_groups[0], 0, True
+    for i, shape in enumerate(_shapes(s)):
+        old, n = group["params"][i], -(-math.prod(shape) // BLOCK) * BLOCK
+        new, state = torch.nn.Parameter(s["p"][at:at + n]), s["opt"].state.pop(old)
+        new.grad = s["g"][at:at + n]
+        group["params"][i] = new
+        s["opt"].state[new] = dict(state, exp_avg=s["m"][at:at + n], exp_avg_sq=s["v"][at:at + n])
+        at += n
 
 
 def _power(k):
