@@ -57,6 +57,7 @@ struct Table {
   int count;
   int64_t chunks;             // of all tensors
   uint32_t* status;
+  uint2 keys[10];             // Philox round keys
   uint32_t id[CAP];           // random stream of each tensor
   int64_t first[CAP];         // first chunk of each tensor
   Tensor t[CAP];
@@ -65,6 +66,7 @@ struct Table {
 // What a step needs of its coefficients, in fp32.
 struct Step {
   float decay, size, rbc2, eps;
+  float b1, a1, b2, a2;   // betas and their complements
   uint32_t t;
 };
 
@@ -86,12 +88,33 @@ __device__ Step make_step(const Coef& c) {
   s.size = (float)(lr / one_minus_power(c.b1, t));
   s.rbc2 = (float)(1.0 / sqrt(one_minus_power(c.b2, t)));
   s.eps = (float)c.eps;
+  s.b1 = (float)c.b1;
+  s.a1 = (float)(1.0 - c.b1);
+  s.b2 = (float)c.b2;
+  s.a2 = (float)(1.0 - c.b2);
   s.t = (uint32_t)t;
   return s;
 }
 
 __device__ __forceinline__ float stepped(float p, float m, float v, const Step& s) {
-  return p * s.decay - s.size * (m / (sqrtf(v) * s.rbc2 + s.eps));
+  float root;
+  asm("sqrt.approx.f32 %0, %1;" : "=f"(root) : "f"(v));   // within 2^-23 of it
+  return p * s.decay - s.size * __fdividef(m, root * s.rbc2 + s.eps);
+}
+
+// The words of one counter (philox10 with its round keys from the table, which saves their sums).
+__device__ __forceinline__ Words4 stream_words(const uint2 (&keys)[10], uint32_t tag, uint32_t step, uint64_t q) {
+  uint32_t c0 = (uint32_t)q, c1 = (uint32_t)(q >> 32), c2 = tag, c3 = step;
+#pragma unroll
+  for (int r = 0; r < 10; ++r) {
+    const uint32_t lo0 = 0xD2511F53u * c0, hi0 = __umulhi(0xD2511F53u, c0);
+    const uint32_t lo1 = 0xCD9E8D57u * c2, hi1 = __umulhi(0xCD9E8D57u, c2);
+    c0 = hi1 ^ c1 ^ keys[r].x;
+    c1 = lo1;
+    c2 = hi0 ^ c3 ^ keys[r].y;
+    c3 = lo0;
+  }
+  return Words4{{c0, c1, c2, c3}};
 }
 
 // Four consecutive elements from i on of a tensor of n; the others read as 0.
@@ -164,20 +187,29 @@ __device__ __forceinline__ void store_codes(uint8_t* a, int64_t i, int64_t n, bo
 }
 
 __device__ __forceinline__ double power2(int e) { return __hiloint2double((e + 1023) << 20, 0); }   // -1022 .. 1023
+__device__ __forceinline__ float power2f(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }   // -126 .. 127
 
+// ---- the moments in fp64, by their definition -------------------------------------
 // A code's magnitude is the fp64 number with bits code << 49 (exponent field code / 8, so
 // that gradual underflow is the format's own) times 2^(1022 + E - 127 - octaves + 1).
-__device__ __forceinline__ double decode(uint32_t code, double scale) {
-  return __hiloint2double((int)(code << 17), 0) * power2(1000) * scale;
+__device__ __forceinline__ double decode64(uint32_t code, int top, int octaves) {
+  return __hiloint2double((int)(code << 17), 0) * power2(1000) * power2(22 + top - octaves + 1);
 }
-__device__ __forceinline__ double decode_scale(int top, int octaves) { return power2(22 + top - octaves + 1); }
+__device__ __forceinline__ double first_moment(uint32_t code, int top, float g, double b1) {
+  const double old = decode64(code & 127u, top, kMOctaves);
+  return __dadd_rn(__dmul_rn(b1, code > 127u ? -old : old), __dmul_rn(1.0 - b1, (double)g));
+}
+__device__ __forceinline__ double second_moment(uint32_t code, int top, float g, double b2) {
+  return __dadd_rn(__dmul_rn(b2, decode64(code, top, kVOctaves)), __dmul_rn(1.0 - b2, __dmul_rn((double)g, (double)g)));
+}
+__device__ __forceinline__ int exponent_field(double x) { return (__double2hiint(x) >> 20) & 0x7FF; }
 
 // The code of a finite x >= 0 from t = x / u.  From 8 on, 3 mantissa bits are kept by an integer
 // addition to the fp64 number (its exponent and upper mantissa bits count the codes); below
 // 8 the grid's step is 1.
 template <bool SR>
-__device__ __forceinline__ uint32_t encode(double x, double per_unit, uint32_t field, uint32_t most) {
-  const double t = x * per_unit;
+__device__ __forceinline__ uint32_t encode64(double x, int top, int octaves, uint32_t field) {
+  const double t = x * power2(octaves + 2 - top);
   if (t < 8.0)
     return (uint32_t)(SR ? __double2int_rd(t + ((double)field + 0.5) * (1.0 / 65536.0)) : __double2int_rn(t));
   const unsigned long long b = (unsigned long long)__double_as_longlong(t);
@@ -186,15 +218,42 @@ __device__ __forceinline__ uint32_t encode(double x, double per_unit, uint32_t f
     r = ((unsigned long long)field << 33) + (1ull << 32);                 // (field + 1/2) 2^-16 of a step
   else
     r = ((1ull << 48) - 1) + ((b >> 49) & 1);                             // nearest, ties to even
-  return min((uint32_t)((b + r) >> 49) - (1026u * 8u - 8u), most);        // 8.0 has the exponent field 1026
+  return min((uint32_t)((b + r) >> 49) - (1026u * 8u - 8u), 8u * octaves + 7u);   // 8.0 has the exponent field 1026
 }
-__device__ __forceinline__ double units(int top, int octaves) { return power2(octaves + 2 - top); }
 
-__device__ __forceinline__ int exponent_field(double x) { return (__double2hiint(x) >> 20) & 0x7FF; }
-
-// Exponent byte - 127 of a block from the largest fp64 exponent field of its elements
-// (0x7FF, a NaN or an infinity, left out by the caller).
+// The same with the block's old and new exponents, for one element.
+template <bool SR>
+__device__ __noinline__ uint32_t exact_codes(uint32_t cm, uint32_t cv, int old_tm, int old_tv, int tm, int tv, float g,
+                                             double b1, double b2, uint32_t word) {
+  const double m = first_moment(cm, old_tm, g, b1), v = second_moment(cv, old_tv, g, b2);
+  // an element whose gradient was not finite (its parameter is NaN now) restarts from zero
+  if (exponent_field(m) == 0x7FF || exponent_field(v) == 0x7FF) return 0u;
+  uint32_t c = encode64<SR>(fabs(m), tm, kMOctaves, word & 0xFFFFu);
+  if (c && m < 0.0) c |= 128u;
+  return c | max(encode64<SR>(v, tv, kVOctaves, word >> 16), v > 0.0 ? 1u : 0u) << 8;
+}
+__device__ __noinline__ float2 exact_moments(uint32_t cm, uint32_t cv, int old_tm, int old_tv, float g, double b1, double b2) {
+  return make_float2((float)first_moment(cm, old_tm, g, b1), (float)second_moment(cv, old_tv, g, b2));
+}
+__device__ __noinline__ uint32_t exact_fields(uint32_t cm, uint32_t cv, int old_tm, int old_tv, float g, double b1, double b2) {
+  const int em = exponent_field(first_moment(cm, old_tm, g, b1)), ev = exponent_field(second_moment(cv, old_tv, g, b2));
+  return (em == 0x7FF ? 0u : (uint32_t)em) | (ev == 0x7FF ? 0u : (uint32_t)ev) << 16;
+}
+// Exponent byte - 127 of a block from the largest fp64 exponent field of its elements.
 __device__ __forceinline__ int block_top(int field) { return min(max(field - 1023, -111), 127); }
+
+// ---- the same in fp32 with a bound on the error -----------------------------------
+// Where both ends of an interval that holds the fp64 value round to the same code, that is the
+// code; elsewhere (one element in 10^5 of an fp32 gradient) the fp64 route decides.  In fp64
+// throughout a step of 71 M elements took 611 us.
+// A magnitude is scaled so that the lowest normal octave of the codes is fp32's own: its bits
+// count the codes in steps of 2^20, gradual underflow included; a unit more or less covers the
+// rounding there.
+template <bool SR>
+__device__ __forceinline__ uint32_t encode32(uint32_t bits, uint32_t field) {
+  if (SR) return (bits + (field << 4) + 8u) >> 20;                        // (field + 1/2) 2^-16 of a step
+  return (bits + 0x7FFFFu + ((bits >> 20) & 1u)) >> 20;                   // nearest, ties to even
+}
 
 template <typename T, int BITS, bool SR, int CAP>
 __global__ void __launch_bounds__(kThreads) adamw_kernel(const __grid_constant__ Table<CAP> tab) {
@@ -221,8 +280,6 @@ __global__ void __launch_bounds__(kThreads) adamw_kernel(const __grid_constant__
       float* m = static_cast<float*>(t.m);
       float* v = static_cast<float*>(t.v);
       const bool vec_s = ((reinterpret_cast<uintptr_t>(m) | reinterpret_cast<uintptr_t>(v)) & 15u) == 0;
-      const float b1 = (float)tab.c.b1, b2 = (float)tab.c.b2;
-      const float a1 = (float)(1.0 - tab.c.b1), a2 = (float)(1.0 - tab.c.b2);
 #pragma unroll
       for (int u = 0; u < kChunk / (kThreads * 4); ++u) {
         const int64_t i = base + (int64_t)(u * kThreads + threadIdx.x) * 4;
@@ -235,8 +292,8 @@ __global__ void __launch_bounds__(kThreads) adamw_kernel(const __grid_constant__
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           bad |= !isfinite(xg[j]);
-          xm[j] = fmaf(b1, xm[j], a1 * xg[j]);
-          xv[j] = fmaf(b2, xv[j], a2 * (xg[j] * xg[j]));
+          xm[j] = fmaf(s.b1, xm[j], s.a1 * xg[j]);
+          xv[j] = fmaf(s.b2, xv[j], s.a2 * (xg[j] * xg[j]));
           xp[j] = stepped(xp[j], xm[j], xv[j], s);
         }
         store4(m, i, n, vec_s, xm);
@@ -245,7 +302,7 @@ __global__ void __launch_bounds__(kThreads) adamw_kernel(const __grid_constant__
           store4(p, i, n, vec_p, xp);
         } else {
           Words4 w{};
-          if (SR) w = stream_call(tab.c.seed, stream_tag(tab.id[lo], kPurposeState, 1), s.t, (uint64_t)i >> 2);
+          if (SR) w = stream_words(tab.keys, stream_tag(tab.id[lo], kPurposeState, 1), s.t, (uint64_t)i >> 2);
           store4(p, i, n, vec_p, xp, SR, w);
         }
       }
@@ -253,7 +310,6 @@ __global__ void __launch_bounds__(kThreads) adamw_kernel(const __grid_constant__
       uint8_t* m = static_cast<uint8_t*>(t.m);
       uint8_t* v = static_cast<uint8_t*>(t.v);
       const bool vec_s = ((reinterpret_cast<uintptr_t>(m) | reinterpret_cast<uintptr_t>(v)) & 3u) == 0;
-      const double b1 = tab.c.b1, b2 = tab.c.b2;
 #pragma unroll
       for (int u = 0; u < kChunk / (kThreads * 4); ++u) {
         // a warp takes one state block
@@ -264,35 +320,89 @@ __global__ void __launch_bounds__(kThreads) adamw_kernel(const __grid_constant__
         load4(p, i, n, vec_p, xp);
         load4(g, i, n, vec_g, xg);
         const uint32_t cm = load_codes(m, i, n, vec_s), cv = load_codes(v, i, n, vec_s);
-        const double dm = decode_scale((int)t.me[blk] - 127, kMOctaves), dv = decode_scale((int)t.ve[blk] - 127, kVOctaves);
-        double ym[4], yv[4];
-        int fm = 0, fv = 0;
+        const int old_tm = (int)t.me[blk] - 127, old_tv = (int)t.ve[blk] - 127;
+        // The fp32 route holds for tops within these, where no scale leaves fp32's range and sums
+        // of a block stay normal; it is left for the fp64 route by an empty interval otherwise.
+        const bool usual = old_tm <= 14 && old_tv <= 30;
+        const float dm = power2f(min(old_tm, 14) + 112), dv = power2f(min(old_tv, 30) + 96);
+        float ym[4], em[4], yv[4];
+        bool odd = false, some = (cm | cv) != 0u;
+        float hm = 0.0f, lm = 0.0f, hv = 0.0f, lv = 0.0f;   // largest upper and lower ends
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           const uint32_t c = (cm >> (8 * j)) & 255u;
-          const double old = decode(c & 127u, dm), gd = (double)xg[j];
-          bad |= !isfinite(xg[j]);
-          ym[j] = __dadd_rn(__dmul_rn(b1, c > 127u ? -old : old), __dmul_rn(1.0 - b1, gd));
-          yv[j] = __dadd_rn(__dmul_rn(b2, decode((cv >> (8 * j)) & 255u, dv)), __dmul_rn(1.0 - b2, __dmul_rn(gd, gd)));
-          const int em = exponent_field(ym[j]), ev = exponent_field(yv[j]);
-          if (em != 0x7FF) fm = max(fm, em);
-          if (ev != 0x7FF) fv = max(fv, ev);
-          xp[j] = stepped(xp[j], (float)ym[j], (float)yv[j], s);
+          const float om = __uint_as_float((c & 127u) << 20) * dm * (c > 127u ? -1.0f : 1.0f);
+          const float ov = __uint_as_float(((cv >> (8 * j)) & 255u) << 20) * dv;
+          odd |= !isfinite(xg[j]);
+          some |= xg[j] != 0.0f;
+          const float sg = s.a1 * xg[j];
+          ym[j] = fmaf(s.b1, om, sg);
+          // 5 2^-24 of the terms: a coefficient's rounding, the product's, the sum's, and those here
+          em[j] = fmaf(s.b1, fabsf(om), fabsf(sg)) * 2.9802322e-7f;
+          // four roundings of 2^-24 or less: 2 units of yv's last place, taken as 4
+          yv[j] = fmaf(s.b2, ov, s.a2 * (xg[j] * xg[j]));
+          if (!usual) {
+            const float2 y = exact_moments(c, (cv >> (8 * j)) & 255u, old_tm, old_tv, xg[j], tab.c.b1, tab.c.b2);
+            ym[j] = y.x;
+            yv[j] = y.y;
+          }
+          hm = fmaxf(hm, fabsf(ym[j]) + em[j]);
+          lm = fmaxf(lm, fabsf(ym[j]) - em[j]);
+          hv = fmaxf(hv, yv[j]);
+          xp[j] = stepped(xp[j], ym[j], yv[j], s);
         }
-        const int tm = block_top(__reduce_max_sync(0xffffffffu, fm)), tv = block_top(__reduce_max_sync(0xffffffffu, fv));
-        const double sm = units(tm, kMOctaves), sv = units(tv, kVOctaves);
+        // the block's exponents, if both ends agree on them (bits of positive floats order like them)
+        const uint32_t top_m = __reduce_max_sync(0xffffffffu, __float_as_uint(hm)), low_m = __reduce_max_sync(0xffffffffu, __float_as_uint(lm));
+        const uint32_t top_v = __reduce_max_sync(0xffffffffu, __float_as_uint(hv));
         Words4 w{};
-        if (SR) w = stream_call(tab.c.seed, stream_tag(tab.id[lo], kPurposeState, 0), s.t, (uint64_t)i >> 2);
-        uint32_t om = 0, ov = 0;
+        if (SR) w = stream_words(tab.keys, stream_tag(tab.id[lo], kPurposeState, 0), s.t, (uint64_t)i >> 2);
+        int tm = (int)(top_m >> 23) - 127, tv = (int)(top_v >> 23) - 127;
+        const uint32_t mv = top_v & 0x7FFFFFu;
+        bad |= odd;
+        const bool open = !usual || __any_sync(0xffffffffu, odd) || (top_m >> 23) != (low_m >> 23) || tm > 14 || tm < -60 || tv > 30 ||
+                    tv < -60 || mv < 8u || mv > 0x7FFFF8u;
+        uint32_t om = 0, ov = 0, redo = 0xFu;
+        if (open) {
+          if (!__any_sync(0xffffffffu, some)) {   // nothing there, and nothing new
+            tm = tv = -111;
+            redo = 0;
+          } else {
+            uint32_t f = 0;
+            for (int j = 0; j < 4; ++j) {
+              const uint32_t e = exact_fields((cm >> (8 * j)) & 255u, (cv >> (8 * j)) & 255u, old_tm, old_tv, xg[j], tab.c.b1, tab.c.b2);
+              f = max(f & 0xFFFFu, e & 0xFFFFu) | max(f >> 16, e >> 16) << 16;
+            }
+            tm = block_top((int)__reduce_max_sync(0xffffffffu, f & 0xFFFFu));
+            tv = block_top((int)__reduce_max_sync(0xffffffffu, f >> 16));
+          }
+        } else {
+          redo = 0;
+          const float sm = power2f(-112 - tm), sv = power2f(-96 - tv);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          uint32_t c = encode<SR>(fabs(ym[j]), sm, w.w[j] & 0xFFFFu, 127u);
-          if (c && ym[j] < 0.0) c |= 128u;
-          uint32_t e = max(encode<SR>(yv[j], sv, w.w[j] >> 16, 255u), yv[j] > 0.0 ? 1u : 0u);
-          // an element whose gradient was not finite (its parameter is NaN now) restarts from zero
-          if (exponent_field(ym[j]) == 0x7FF || exponent_field(yv[j]) == 0x7FF) c = e = 0;
-          om |= c << (8 * j);
-          ov |= e << (8 * j);
+          for (int j = 0; j < 4; ++j) {
+            const float a = fabsf(ym[j]);
+            const uint32_t c = encode32<SR>(__float_as_uint((a + em[j]) * sm) + 1u, w.w[j] & 0xFFFFu);
+            const uint32_t bl = __float_as_uint(fmaxf(a - em[j], 0.0f) * sm);
+            const uint32_t c_low = encode32<SR>(bl - (bl ? 1u : 0u), w.w[j] & 0xFFFFu);
+            const uint32_t bv = __float_as_uint(yv[j] * sv);
+            const uint32_t e = encode32<SR>(bv + 4u, w.w[j] >> 16), e_low = encode32<SR>(bv - min(bv, 4u), w.w[j] >> 16);
+            if (c != c_low || e != e_low) redo |= 1u << j;
+            const uint32_t cs = min(c, 127u) | (c && ym[j] < 0.0f ? 128u : 0u);
+            om |= cs << (8 * j);
+            // v > 0 in fp64, where fp32 may have lost it
+            const bool positive = xg[j] != 0.0f || (s.b2 > 0.0f && ((cv >> (8 * j)) & 255u));
+            ov |= max(min(e, 255u), positive ? 1u : 0u) << (8 * j);
+          }
+        }
+        while (redo) {
+          const int j = __ffs(redo) - 1;
+          redo &= redo - 1;
+          const uint32_t word = j == 0 ? w.w[0] : j == 1 ? w.w[1] : j == 2 ? w.w[2] : w.w[3];
+          const float gj = j == 0 ? xg[0] : j == 1 ? xg[1] : j == 2 ? xg[2] : xg[3];
+          const uint32_t c = exact_codes<SR>((cm >> (8 * j)) & 255u, (cv >> (8 * j)) & 255u, old_tm, old_tv, tm, tv, gj, tab.c.b1,
+                                             tab.c.b2, word);
+          om = (om & ~(255u << (8 * j))) | (c & 255u) << (8 * j);
+          ov = (ov & ~(255u << (8 * j))) | (c >> 8) << (8 * j);
         }
         store_codes(m, i, n, vec_s, om);
         store_codes(v, i, n, vec_s, ov);
@@ -304,7 +414,7 @@ __global__ void __launch_bounds__(kThreads) adamw_kernel(const __grid_constant__
           store4(p, i, n, vec_p, xp);
         } else {
           Words4 wp{};
-          if (SR) wp = stream_call(tab.c.seed, stream_tag(tab.id[lo], kPurposeState, 1), s.t, (uint64_t)i >> 2);
+          if (SR) wp = stream_words(tab.keys, stream_tag(tab.id[lo], kPurposeState, 1), s.t, (uint64_t)i >> 2);
           store4(p, i, n, vec_p, xp, SR, wp);
         }
       }
@@ -318,6 +428,8 @@ cudaError_t launch_cap(metis_ctx* ctx, const metis_adamw_tensor* const* ts, int 
   static thread_local Table<CAP> tab;
   tab.c = c;
   tab.status = ctx->status;
+  for (uint32_t r = 0; r < 10; ++r)
+    tab.keys[r] = make_uint2((uint32_t)c.seed + r * 0x9E3779B9u, (uint32_t)(c.seed >> 32) + r * 0xBB67AE85u);
   int64_t chunks = 0;
   for (int i = 0; i < count; ++i) {
     const metis_adamw_tensor& x = *ts[i];

@@ -224,9 +224,9 @@ __device__ __noinline__ Chunk<T> mark_nonfinite(Chunk<T> k, int c, uint32_t* mar
 
 // Threads of a block (several groups) and blocks of an SM: what the registers allow.
 template <int GROUP, bool TOPS>
-constexpr int kRowBlock = TOPS ? 512 : GROUP == 32 ? kThreads : GROUP;
+constexpr int kRowBlock = TOPS ? (GROUP == 512 ? 512 : 256) : GROUP == 32 ? kThreads : GROUP;
 template <typename T, int GROUP, int HELD, bool TOPS>
-constexpr int kRowBlocks = (HELD * (int)sizeof(T) == 16 ? 640 : 1024) / kRowBlock<GROUP, TOPS>;
+constexpr int kRowBlocks = (HELD * (int)sizeof(T) == 16 ? 640 : TOPS ? 768 : 1024) / kRowBlock<GROUP, TOPS>;
 
 template <typename T, int GROUP, int HELD, bool TOPS>
 __global__ void __launch_bounds__(kRowBlock<GROUP, TOPS>, kRowBlocks<T, GROUP, HELD, TOPS>)
@@ -384,7 +384,7 @@ __device__ __forceinline__ void copy_async16(void* dst, const void* src) {
 __device__ __forceinline__ void copy_async_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 
 template <typename T>
-__global__ void __launch_bounds__(kThreads, 5) quantize_i8_cols_kernel(const T* __restrict__ M, int64_t rows, int64_t cols,
+__global__ void __launch_bounds__(kThreads, 4) quantize_i8_cols_kernel(const T* __restrict__ M, int64_t rows, int64_t cols,
                                                                        int64_t ld, int8_t* __restrict__ codes, int64_t ldq,
                                                                        float* __restrict__ scales, const uint32_t* tops,
                                                                        const uint32_t* marks) {
