@@ -29,7 +29,7 @@ namespace metis {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kChunk = 2048;          // elements a block handles at a time: 16 state blocks
+constexpr int kUnit = 1024;           // elements a block takes at once: a state block for each warp
 constexpr int kStateBlock = 128;      // elements that share an exponent
 constexpr int kMOctaves = 15, kVOctaves = 31;
 
@@ -56,6 +56,7 @@ struct Table {
   Coef c;
   int count;
   int64_t chunks;             // of all tensors
+  int units;                  // of a chunk, which a block handles at a time
   uint32_t* status;
   uint2 keys[10];             // Philox round keys
   uint32_t id[CAP];           // random stream of each tensor
@@ -248,20 +249,210 @@ __device__ __forceinline__ int block_top(int field) { return min(max(field - 102
 // throughout a step of 71 M elements took 611 us.
 // A magnitude is scaled so that the lowest normal octave of the codes is fp32's own: its bits
 // count the codes in steps of 2^20, gradual underflow included; a unit more or less covers the
-// rounding there.
+// rounding there.  What an addition to the bits has to carry to round up:
+//   stochastic: (field + 1/2) 2^-16 of a step; nearest: half a step, less a unit unless the code is odd.
 template <bool SR>
-__device__ __forceinline__ uint32_t encode32(uint32_t bits, uint32_t field) {
-  if (SR) return (bits + (field << 4) + 8u) >> 20;                        // (field + 1/2) 2^-16 of a step
-  return (bits + 0x7FFFFu + ((bits >> 20) & 1u)) >> 20;                   // nearest, ties to even
+__device__ __forceinline__ uint32_t carry_of(uint32_t field16, uint32_t bits) {
+  return SR ? field16 << 4 | 8u : 0x7FFFFu + ((bits >> 20) & 1u);
+}
+
+// One state block of 128 elements in a warp, four to a lane.
+struct Block4 {
+  float p[4], g[4];
+  uint32_t cm, cv;
+  int tm, tv;      // exponent bytes - 127
+};
+
+// Steps the block's parameters in place and gives its new codes and exponents.  Returns whether a
+// gradient of the lane is not finite.
+template <bool SR>
+__device__ __forceinline__ bool step_block(Block4& x, const Step& s, double b1, double b2, const Words4& w) {
+  // The fp32 route holds for exponents within these, where no scale leaves fp32's range and a
+  // block's sums stay normal.
+  const bool usual = x.tm <= 14 && x.tv <= 30;
+  const float dm = power2f(min(x.tm, 14) + 112), dv = power2f(min(x.tv, 30) + 96);
+  float ym[4], em[4], yv[4];
+  float hm = 0.0f, lm = 0.0f, hv = 0.0f, z = 0.0f;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const uint32_t mag = (j < 3 ? x.cm << (20 - 8 * j) : x.cm >> 4) & 0x07F00000u, neg = (x.cm << (24 - 8 * j)) & 0x80000000u;
+    const uint32_t vbits = (j < 3 ? x.cv << (20 - 8 * j) : x.cv >> 4) & 0x0FF00000u;
+    const float om = __uint_as_float(__float_as_uint(__uint_as_float(mag) * dm) | neg);
+    const float sg = s.a1 * x.g[j];
+    z = fmaf(x.g[j], 0.0f, z);                       // NaN if any is not finite
+    ym[j] = fmaf(s.b1, om, sg);
+    // 5 2^-24 of the terms: a coefficient's rounding, the product's, the sum's, and those here
+    em[j] = fmaf(s.b1, fabsf(om), fabsf(sg)) * 2.9802322e-7f;
+    // four roundings of 2^-24 or less: 2 units of yv's last place, taken as 4
+    yv[j] = fmaf(s.b2, __uint_as_float(vbits) * dv, s.a2 * (x.g[j] * x.g[j]));
+    if (!usual) {
+      const float2 y = exact_moments((x.cm >> (8 * j)) & 255u, (x.cv >> (8 * j)) & 255u, x.tm, x.tv, x.g[j], b1, b2);
+      ym[j] = y.x;
+      yv[j] = y.y;
+    }
+    hm = fmaxf(hm, fabsf(ym[j]) + em[j]);
+    lm = fmaxf(lm, fabsf(ym[j]) - em[j]);
+    hv = fmaxf(hv, yv[j]);
+    x.p[j] = stepped(x.p[j], ym[j], yv[j], s);
+  }
+  // the block's exponents, if both ends agree on them (bits of positive floats order like them)
+  const uint32_t top_m = __reduce_max_sync(0xffffffffu, __float_as_uint(hm)), low_m = __reduce_max_sync(0xffffffffu, __float_as_uint(lm));
+  const uint32_t top_v = __reduce_max_sync(0xffffffffu, __float_as_uint(hv));
+  int tm = (int)(top_m >> 23) - 127, tv = (int)(top_v >> 23) - 127;
+  const uint32_t edge = ((top_v & 0x7FFFFFu) + 8u) & 0x7FFFFFu;   // below 16: within 8 units of a power of two
+  const bool odd = z != z;
+  const bool open = !usual || __any_sync(0xffffffffu, odd) || ((top_m ^ low_m) >> 23) != 0u || tm > 14 || tm < -60 || tv > 30 ||
+                    tv < -60 || edge < 16u;
+  uint32_t om = 0, ov = 0, redo = 0;
+  if (open) {
+    const bool some = (x.cm | x.cv) != 0u || x.g[0] != 0.0f || x.g[1] != 0.0f || x.g[2] != 0.0f || x.g[3] != 0.0f;
+    if (!__any_sync(0xffffffffu, some)) {   // nothing there, and nothing new
+      tm = tv = -111;
+    } else {
+      uint32_t f = 0;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const uint32_t e = exact_fields((x.cm >> (8 * j)) & 255u, (x.cv >> (8 * j)) & 255u, x.tm, x.tv, x.g[j], b1, b2);
+        f = max(f & 0xFFFFu, e & 0xFFFFu) | max(f >> 16, e >> 16) << 16;
+      }
+      tm = block_top((int)__reduce_max_sync(0xffffffffu, f & 0xFFFFu));
+      tv = block_top((int)__reduce_max_sync(0xffffffffu, f >> 16));
+      redo = 0xFu;
+    }
+  } else {
+    const float sm = power2f(-112 - tm), sv = power2f(-96 - tv);
+    uint32_t cm[4], cv[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const float a = fabsf(ym[j]);
+      const uint32_t bh = __float_as_uint((a + em[j]) * sm), bl = __float_as_uint(fmaxf(a - em[j], 0.0f) * sm);
+      const uint32_t high = bh + carry_of<SR>(w.w[j] & 0xFFFFu, bh) + 1u, low = bl + carry_of<SR>(w.w[j] & 0xFFFFu, bl) - 1u;
+      const uint32_t bv = __float_as_uint(yv[j] * sv);
+      const uint32_t carry = carry_of<SR>(w.w[j] >> 16, bv);
+      // the low end of v: its own carry would differ from this one only across a code's border,
+      // and then the codes differ
+      const uint32_t vh = bv + carry + 4u, vl = bv + carry - 4u;
+      if (((high ^ low) | (vh ^ vl)) >> 20) redo |= 1u << j;
+      if (yv[j] == 0.0f && (x.g[j] != 0.0f || (x.cv >> (8 * j)) & 255u)) redo |= 1u << j;   // fp64 may see more
+      cm[j] = min(high >> 20, 127u);
+      cm[j] |= cm[j] ? (__float_as_uint(ym[j]) >> 24) & 128u : 0u;
+      cv[j] = max(min(vh >> 20, 255u), min(__float_as_uint(yv[j]), 1u));
+    }
+    om = __byte_perm(__byte_perm(cm[0], cm[1], 0x0040), __byte_perm(cm[2], cm[3], 0x0040), 0x5410);
+    ov = __byte_perm(__byte_perm(cv[0], cv[1], 0x0040), __byte_perm(cv[2], cv[3], 0x0040), 0x5410);
+  }
+  while (redo) {
+    const int j = __ffs(redo) - 1;
+    redo &= redo - 1;
+    const uint32_t word = j == 0 ? w.w[0] : j == 1 ? w.w[1] : j == 2 ? w.w[2] : w.w[3];
+    const float gj = j == 0 ? x.g[0] : j == 1 ? x.g[1] : j == 2 ? x.g[2] : x.g[3];
+    const uint32_t c = exact_codes<SR>((x.cm >> (8 * j)) & 255u, (x.cv >> (8 * j)) & 255u, x.tm, x.tv, tm, tv, gj, b1, b2, word);
+    om = (om & ~(255u << (8 * j))) | (c & 255u) << (8 * j);
+    ov = (ov & ~(255u << (8 * j))) | (c >> 8) << (8 * j);
+  }
+  x.cm = om;
+  x.cv = ov;
+  x.tm = tm;
+  x.tv = tv;
+  return odd;
+}
+
+// A tensor's arrays as the kernel walks them.  FAST: all are aligned and the chunk lies inside.
+template <typename T, bool FAST>
+struct View {
+  T* p;
+  const T* g;
+  void* m;
+  void* v;
+  int64_t n;
+  bool vec_p, vec_g, vec_s;
+  __device__ __forceinline__ bool in(int64_t i) const { return FAST || i < n; }
+  __device__ __forceinline__ void load(int64_t i, float (&xp)[4], float (&xg)[4]) const {
+    load4(p, i, FAST ? i + 4 : n, FAST || vec_p, xp);
+    load4(g, i, FAST ? i + 4 : n, FAST || vec_g, xg);
+  }
+  __device__ __forceinline__ void store(int64_t i, const float (&xp)[4], bool sr, const Words4& w) const {
+    if constexpr (sizeof(T) == 4) store4(p, i, FAST ? i + 4 : n, FAST || vec_p, xp);
+    else store4(p, i, FAST ? i + 4 : n, FAST || vec_p, xp, sr, w);
+  }
+};
+
+// One chunk (elements base .. base + units * kUnit of a tensor).  Returns whether a gradient of the
+// thread is not finite.
+template <typename T, int BITS, bool SR, bool FAST, int CAP>
+__device__ __forceinline__ bool run_chunk(const Table<CAP>& tab, int which, int64_t base, const View<T, FAST>& a, const Step& s) {
+  bool bad = false;
+  const uint32_t tag = stream_tag(tab.id[which], kPurposeState, 0);
+  if constexpr (BITS == 32) {
+    float* m = static_cast<float*>(a.m);
+    float* v = static_cast<float*>(a.v);
+    int64_t i = base + (int64_t)threadIdx.x * 4;
+#pragma unroll 2
+    for (int u = 0; u < tab.units; ++u, i += kUnit) {
+      if (!a.in(i)) break;
+      float xp[4], xg[4], xm[4], xv[4], z = 0.0f;
+      a.load(i, xp, xg);
+      load4(m, i, FAST ? i + 4 : a.n, FAST || a.vec_s, xm);
+      load4(v, i, FAST ? i + 4 : a.n, FAST || a.vec_s, xv);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        z = fmaf(xg[j], 0.0f, z);
+        xm[j] = fmaf(s.b1, xm[j], s.a1 * xg[j]);
+        xv[j] = fmaf(s.b2, xv[j], s.a2 * (xg[j] * xg[j]));
+        xp[j] = stepped(xp[j], xm[j], xv[j], s);
+      }
+      bad |= z != z;
+      store4(m, i, FAST ? i + 4 : a.n, FAST || a.vec_s, xm);
+      store4(v, i, FAST ? i + 4 : a.n, FAST || a.vec_s, xv);
+      Words4 w{};
+      if (SR && sizeof(T) == 2) w = stream_words(tab.keys, tag | 1u, s.t, (uint64_t)i >> 2);
+      a.store(i, xp, SR, w);
+    }
+  } else {
+    uint8_t* m = static_cast<uint8_t*>(a.m);
+    uint8_t* v = static_cast<uint8_t*>(a.v);
+    uint8_t* me = tab.t[which].me;
+    uint8_t* ve = tab.t[which].ve;
+    const int lane = threadIdx.x & 31;
+    int64_t i = base + (int64_t)threadIdx.x * 4;   // a warp takes one state block of each unit
+    auto load = [&](int64_t i, Block4& x) {
+      a.load(i, x.p, x.g);
+      x.cm = load_codes(m, i, FAST ? i + 4 : a.n, FAST || a.vec_s);
+      x.cv = load_codes(v, i, FAST ? i + 4 : a.n, FAST || a.vec_s);
+      const int64_t blk = i / kStateBlock;
+      x.tm = (int)me[blk] - 127;
+      x.tv = (int)ve[blk] - 127;
+    };
+    const int64_t first = i - lane * 4;            // of the warp's block
+    Block4 next;
+    if (a.in(first)) load(i, next);
+    for (int u = 0; u < tab.units; ++u, i += kUnit) {
+      if (!a.in(i - lane * 4)) break;
+      Block4 x = next;
+      if (u + 1 < tab.units && a.in(i - lane * 4 + kUnit)) load(i + kUnit, next);
+      Words4 w{};
+      if (SR) w = stream_words(tab.keys, tag, s.t, (uint64_t)i >> 2);
+      bad |= step_block<SR>(x, s, tab.c.b1, tab.c.b2, w);
+      store_codes(m, i, FAST ? i + 4 : a.n, FAST || a.vec_s, x.cm);
+      store_codes(v, i, FAST ? i + 4 : a.n, FAST || a.vec_s, x.cv);
+      if (lane == 0) {
+        me[i / kStateBlock] = (uint8_t)(x.tm + 127);
+        ve[i / kStateBlock] = (uint8_t)(x.tv + 127);
+      }
+      Words4 wp{};
+      if (SR && sizeof(T) == 2) wp = stream_words(tab.keys, tag | 1u, s.t, (uint64_t)i >> 2);
+      a.store(i, x.p, SR, wp);
+    }
+  }
+  return bad;
 }
 
 template <typename T, int BITS, bool SR, int CAP>
-__global__ void __launch_bounds__(kThreads) adamw_kernel(const __grid_constant__ Table<CAP> tab) {
+__global__ void __launch_bounds__(kThreads, BITS == 32 ? 5 : 3) adamw_kernel(const __grid_constant__ Table<CAP> tab) {
   __shared__ Step sh;
   if (threadIdx.x == 0) sh = make_step(tab.c);
   __syncthreads();
   const Step s = sh;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   bool bad = false;
   for (int64_t chunk = blockIdx.x; chunk < tab.chunks; chunk += gridDim.x) {
     int lo = 0, hi = tab.count - 1;   // the last tensor whose first chunk is not beyond this one
@@ -270,155 +461,14 @@ __global__ void __launch_bounds__(kThreads) adamw_kernel(const __grid_constant__
       if (tab.first[mid] <= chunk) lo = mid; else hi = mid - 1;
     }
     const Tensor& t = tab.t[lo];
-    const int64_t n = t.n;
-    const int64_t base = (chunk - tab.first[lo]) * kChunk;
-    T* p = static_cast<T*>(t.p);
-    const T* g = static_cast<const T*>(t.g);
-    const uintptr_t mask = sizeof(T) == 4 ? 15u : 7u;
-    const bool vec_p = (reinterpret_cast<uintptr_t>(p) & mask) == 0, vec_g = (reinterpret_cast<uintptr_t>(g) & mask) == 0;
-    if constexpr (BITS == 32) {
-      float* m = static_cast<float*>(t.m);
-      float* v = static_cast<float*>(t.v);
-      const bool vec_s = ((reinterpret_cast<uintptr_t>(m) | reinterpret_cast<uintptr_t>(v)) & 15u) == 0;
-#pragma unroll
-      for (int u = 0; u < kChunk / (kThreads * 4); ++u) {
-        const int64_t i = base + (int64_t)(u * kThreads + threadIdx.x) * 4;
-        if (i >= n) continue;
-        float xp[4], xg[4], xm[4], xv[4];
-        load4(p, i, n, vec_p, xp);
-        load4(g, i, n, vec_g, xg);
-        load4(m, i, n, vec_s, xm);
-        load4(v, i, n, vec_s, xv);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          bad |= !isfinite(xg[j]);
-          xm[j] = fmaf(s.b1, xm[j], s.a1 * xg[j]);
-          xv[j] = fmaf(s.b2, xv[j], s.a2 * (xg[j] * xg[j]));
-          xp[j] = stepped(xp[j], xm[j], xv[j], s);
-        }
-        store4(m, i, n, vec_s, xm);
-        store4(v, i, n, vec_s, xv);
-        if constexpr (sizeof(T) == 4) {
-          store4(p, i, n, vec_p, xp);
-        } else {
-          Words4 w{};
-          if (SR) w = stream_words(tab.keys, stream_tag(tab.id[lo], kPurposeState, 1), s.t, (uint64_t)i >> 2);
-          store4(p, i, n, vec_p, xp, SR, w);
-        }
-      }
-    } else {
-      uint8_t* m = static_cast<uint8_t*>(t.m);
-      uint8_t* v = static_cast<uint8_t*>(t.v);
-      const bool vec_s = ((reinterpret_cast<uintptr_t>(m) | reinterpret_cast<uintptr_t>(v)) & 3u) == 0;
-#pragma unroll
-      for (int u = 0; u < kChunk / (kThreads * 4); ++u) {
-        // a warp takes one state block
-        const int64_t i0 = base + (int64_t)(u * (kThreads / 32) + warp) * kStateBlock;
-        if (i0 >= n) break;
-        const int64_t i = i0 + lane * 4, blk = i0 / kStateBlock;
-        float xp[4], xg[4];
-        load4(p, i, n, vec_p, xp);
-        load4(g, i, n, vec_g, xg);
-        const uint32_t cm = load_codes(m, i, n, vec_s), cv = load_codes(v, i, n, vec_s);
-        const int old_tm = (int)t.me[blk] - 127, old_tv = (int)t.ve[blk] - 127;
-        // The fp32 route holds for tops within these, where no scale leaves fp32's range and sums
-        // of a block stay normal; it is left for the fp64 route by an empty interval otherwise.
-        const bool usual = old_tm <= 14 && old_tv <= 30;
-        const float dm = power2f(min(old_tm, 14) + 112), dv = power2f(min(old_tv, 30) + 96);
-        float ym[4], em[4], yv[4];
-        bool odd = false, some = (cm | cv) != 0u;
-        float hm = 0.0f, lm = 0.0f, hv = 0.0f, lv = 0.0f;   // largest upper and lower ends
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const uint32_t c = (cm >> (8 * j)) & 255u;
-          const float om = __uint_as_float((c & 127u) << 20) * dm * (c > 127u ? -1.0f : 1.0f);
-          const float ov = __uint_as_float(((cv >> (8 * j)) & 255u) << 20) * dv;
-          odd |= !isfinite(xg[j]);
-          some |= xg[j] != 0.0f;
-          const float sg = s.a1 * xg[j];
-          ym[j] = fmaf(s.b1, om, sg);
-          // 5 2^-24 of the terms: a coefficient's rounding, the product's, the sum's, and those here
-          em[j] = fmaf(s.b1, fabsf(om), fabsf(sg)) * 2.9802322e-7f;
-          // four roundings of 2^-24 or less: 2 units of yv's last place, taken as 4
-          yv[j] = fmaf(s.b2, ov, s.a2 * (xg[j] * xg[j]));
-          if (!usual) {
-            const float2 y = exact_moments(c, (cv >> (8 * j)) & 255u, old_tm, old_tv, xg[j], tab.c.b1, tab.c.b2);
-            ym[j] = y.x;
-            yv[j] = y.y;
-          }
-          hm = fmaxf(hm, fabsf(ym[j]) + em[j]);
-          lm = fmaxf(lm, fabsf(ym[j]) - em[j]);
-          hv = fmaxf(hv, yv[j]);
-          xp[j] = stepped(xp[j], ym[j], yv[j], s);
-        }
-        // the block's exponents, if both ends agree on them (bits of positive floats order like them)
-        const uint32_t top_m = __reduce_max_sync(0xffffffffu, __float_as_uint(hm)), low_m = __reduce_max_sync(0xffffffffu, __float_as_uint(lm));
-        const uint32_t top_v = __reduce_max_sync(0xffffffffu, __float_as_uint(hv));
-        Words4 w{};
-        if (SR) w = stream_words(tab.keys, stream_tag(tab.id[lo], kPurposeState, 0), s.t, (uint64_t)i >> 2);
-        int tm = (int)(top_m >> 23) - 127, tv = (int)(top_v >> 23) - 127;
-        const uint32_t mv = top_v & 0x7FFFFFu;
-        bad |= odd;
-        const bool open = !usual || __any_sync(0xffffffffu, odd) || (top_m >> 23) != (low_m >> 23) || tm > 14 || tm < -60 || tv > 30 ||
-                    tv < -60 || mv < 8u || mv > 0x7FFFF8u;
-        uint32_t om = 0, ov = 0, redo = 0xFu;
-        if (open) {
-          if (!__any_sync(0xffffffffu, some)) {   // nothing there, and nothing new
-            tm = tv = -111;
-            redo = 0;
-          } else {
-            uint32_t f = 0;
-            for (int j = 0; j < 4; ++j) {
-              const uint32_t e = exact_fields((cm >> (8 * j)) & 255u, (cv >> (8 * j)) & 255u, old_tm, old_tv, xg[j], tab.c.b1, tab.c.b2);
-              f = max(f & 0xFFFFu, e & 0xFFFFu) | max(f >> 16, e >> 16) << 16;
-            }
-            tm = block_top((int)__reduce_max_sync(0xffffffffu, f & 0xFFFFu));
-            tv = block_top((int)__reduce_max_sync(0xffffffffu, f >> 16));
-          }
-        } else {
-          redo = 0;
-          const float sm = power2f(-112 - tm), sv = power2f(-96 - tv);
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const float a = fabsf(ym[j]);
-            const uint32_t c = encode32<SR>(__float_as_uint((a + em[j]) * sm) + 1u, w.w[j] & 0xFFFFu);
-            const uint32_t bl = __float_as_uint(fmaxf(a - em[j], 0.0f) * sm);
-            const uint32_t c_low = encode32<SR>(bl - (bl ? 1u : 0u), w.w[j] & 0xFFFFu);
-            const uint32_t bv = __float_as_uint(yv[j] * sv);
-            const uint32_t e = encode32<SR>(bv + 4u, w.w[j] >> 16), e_low = encode32<SR>(bv - min(bv, 4u), w.w[j] >> 16);
-            if (c != c_low || e != e_low) redo |= 1u << j;
-            const uint32_t cs = min(c, 127u) | (c && ym[j] < 0.0f ? 128u : 0u);
-            om |= cs << (8 * j);
-            // v > 0 in fp64, where fp32 may have lost it
-            const bool positive = xg[j] != 0.0f || (s.b2 > 0.0f && ((cv >> (8 * j)) & 255u));
-            ov |= max(min(e, 255u), positive ? 1u : 0u) << (8 * j);
-          }
-        }
-        while (redo) {
-          const int j = __ffs(redo) - 1;
-          redo &= redo - 1;
-          const uint32_t word = j == 0 ? w.w[0] : j == 1 ? w.w[1] : j == 2 ? w.w[2] : w.w[3];
-          const float gj = j == 0 ? xg[0] : j == 1 ? xg[1] : j == 2 ? xg[2] : xg[3];
-          const uint32_t c = exact_codes<SR>((cm >> (8 * j)) & 255u, (cv >> (8 * j)) & 255u, old_tm, old_tv, tm, tv, gj, tab.c.b1,
-                                             tab.c.b2, word);
-          om = (om & ~(255u << (8 * j))) | (c & 255u) << (8 * j);
-          ov = (ov & ~(255u << (8 * j))) | (c >> 8) << (8 * j);
-        }
-        store_codes(m, i, n, vec_s, om);
-        store_codes(v, i, n, vec_s, ov);
-        if (lane == 0) {
-          t.me[blk] = (uint8_t)(tm + 127);
-          t.ve[blk] = (uint8_t)(tv + 127);
-        }
-        if constexpr (sizeof(T) == 4) {
-          store4(p, i, n, vec_p, xp);
-        } else {
-          Words4 wp{};
-          if (SR) wp = stream_words(tab.keys, stream_tag(tab.id[lo], kPurposeState, 1), s.t, (uint64_t)i >> 2);
-          store4(p, i, n, vec_p, xp, SR, wp);
-        }
-      }
-    }
+    const int64_t base = (chunk - tab.first[lo]) * tab.units * kUnit;
+    const uintptr_t mask = sizeof(T) == 4 ? 15u : 7u, state_mask = BITS == 32 ? 15u : 3u;
+    const bool vec_p = (reinterpret_cast<uintptr_t>(t.p) & mask) == 0, vec_g = (reinterpret_cast<uintptr_t>(t.g) & mask) == 0;
+    const bool vec_s = ((reinterpret_cast<uintptr_t>(t.m) | reinterpret_cast<uintptr_t>(t.v)) & state_mask) == 0;
+    if (vec_p && vec_g && vec_s && base + (int64_t)tab.units * kUnit <= t.n)
+      bad |= run_chunk<T, BITS, SR>(tab, lo, base, View<T, true>{static_cast<T*>(t.p), static_cast<const T*>(t.g), t.m, t.v, t.n, true, true, true}, s);
+    else
+      bad |= run_chunk<T, BITS, SR>(tab, lo, base, View<T, false>{static_cast<T*>(t.p), static_cast<const T*>(t.g), t.m, t.v, t.n, vec_p, vec_g, vec_s}, s);
   }
   if (bad) raise_status(tab.status, METIS_DEV_NONFINITE);
 }
@@ -430,17 +480,23 @@ cudaError_t launch_cap(metis_ctx* ctx, const metis_adamw_tensor* const* ts, int 
   tab.status = ctx->status;
   for (uint32_t r = 0; r < 10; ++r)
     tab.keys[r] = make_uint2((uint32_t)c.seed + r * 0x9E3779B9u, (uint32_t)(c.seed >> 32) + r * 0xBB67AE85u);
-  int64_t chunks = 0;
+  // Chunks as large as leave every SM eight of them: the search for a chunk's tensor and the
+  // tensor's addresses are paid once a chunk.
+  int64_t elements = 0, chunks = 0;
+  for (int i = 0; i < count; ++i) elements += ts[i]->n;
+  tab.units = 1;
+  while (tab.units < 16 && elements / (2 * tab.units * kUnit) >= 8 * (int64_t)ctx->sm_count) tab.units *= 2;
+  const int64_t chunk = (int64_t)tab.units * kUnit;
   for (int i = 0; i < count; ++i) {
     const metis_adamw_tensor& x = *ts[i];
     tab.t[i] = Tensor{x.p, x.g, x.m, x.v, x.m_exponent, x.v_exponent, x.n};
     tab.id[i] = x.id;
     tab.first[i] = chunks;
-    chunks += (x.n + kChunk - 1) / kChunk;
+    chunks += (x.n + chunk - 1) / chunk;
   }
   tab.count = count;
   tab.chunks = chunks;
-  const int64_t grid = std::min<int64_t>(chunks, (int64_t)ctx->sm_count * 8);
+  const int64_t grid = std::min<int64_t>(chunks, (int64_t)ctx->sm_count * (BITS == 32 ? 5 : 3));
   adamw_kernel<T, BITS, SR, CAP><<<(unsigned)grid, kThreads, 0, ctx->stream>>>(tab);
   count_launch();
   return cudaGetLastError();
