@@ -67,7 +67,10 @@ struct Table {
 // What a step needs of its coefficients, in fp32.
 struct Step {
   float decay, size, rbc2, eps;
-  float b1, a1, b2, a2;   // betas and their complements
+  float b1, b1_low;       // beta1: its upper 20 bits and the rest
+  float a1, a1_low;       // 1 - beta1: nearest and the rest
+  float b2, a2;           // beta2 and 1 - beta2
+  bool tiny;              // eps does not hide the root of a subnormal v
   uint32_t t;
 };
 
@@ -89,18 +92,30 @@ __device__ Step make_step(const Coef& c) {
   s.size = (float)(lr / one_minus_power(c.b1, t));
   s.rbc2 = (float)(1.0 / sqrt(one_minus_power(c.b2, t)));
   s.eps = (float)c.eps;
-  s.b1 = (float)c.b1;
+  s.b1 = __uint_as_float(__float_as_uint((float)c.b1) & ~15u);
+  s.b1_low = (float)(c.b1 - (double)s.b1);
   s.a1 = (float)(1.0 - c.b1);
+  s.a1_low = (float)((1.0 - c.b1) - (double)s.a1);
+  s.tiny = !(c.eps >= 1e-11);
   s.b2 = (float)c.b2;
   s.a2 = (float)(1.0 - c.b2);
   s.t = (uint32_t)t;
   return s;
 }
 
+// Root and reciprocal within 2^-23 and 2^-22.  Flushing a subnormal v (root below 2^-63) to 0 does
+// not show beside an eps of 1e-11; with a smaller one the slower forms keep it.
 __device__ __forceinline__ float stepped(float p, float m, float v, const Step& s) {
-  float root;
-  asm("sqrt.approx.f32 %0, %1;" : "=f"(root) : "f"(v));   // within 2^-23 of it
-  return p * s.decay - s.size * __fdividef(m, root * s.rbc2 + s.eps);
+  float root, q;
+  if (!s.tiny) {
+    asm("sqrt.approx.ftz.f32 %0, %1;" : "=f"(root) : "f"(v));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(q) : "f"(fmaf(root, s.rbc2, s.eps)));
+    q *= m;
+  } else {
+    asm("sqrt.approx.f32 %0, %1;" : "=f"(root) : "f"(v));
+    q = __fdiv_rn(m, fmaf(root, s.rbc2, s.eps));
+  }
+  return fmaf(-s.size, q, p * s.decay);
 }
 
 // The words of one counter (philox10 with its round keys from the table, which saves their sums).
@@ -108,32 +123,48 @@ __device__ __forceinline__ Words4 stream_words(const uint2 (&keys)[10], uint32_t
   uint32_t c0 = (uint32_t)q, c1 = (uint32_t)(q >> 32), c2 = tag, c3 = step;
 #pragma unroll
   for (int r = 0; r < 10; ++r) {
-    const uint32_t lo0 = 0xD2511F53u * c0, hi0 = __umulhi(0xD2511F53u, c0);
-    const uint32_t lo1 = 0xCD9E8D57u * c2, hi1 = __umulhi(0xCD9E8D57u, c2);
-    c0 = hi1 ^ c1 ^ keys[r].x;
-    c1 = lo1;
-    c2 = hi0 ^ c3 ^ keys[r].y;
-    c3 = lo0;
+    const uint64_t a = (uint64_t)0xD2511F53u * c0, b = (uint64_t)0xCD9E8D57u * c2;
+    c0 = (uint32_t)(b >> 32) ^ c1 ^ keys[r].x;
+    c1 = (uint32_t)b;
+    c2 = (uint32_t)(a >> 32) ^ c3 ^ keys[r].y;
+    c3 = (uint32_t)a;
   }
   return Words4{{c0, c1, c2, c3}};
 }
 
-// Four consecutive elements from i on of a tensor of n; the others read as 0.
+// Four consecutive elements as they are in memory; unpacked where they are used, so that a load
+// ahead is not waited for.
 template <typename T>
-__device__ __forceinline__ void load4(const T* a, int64_t i, int64_t n, bool vec, float (&x)[4]) {
+struct Four {
+  uint32_t w[(int)sizeof(T)];
+  __device__ __forceinline__ float get(int j) const {
+    if constexpr (sizeof(T) == 4) return __uint_as_float(w[j]);
+    else return __uint_as_float((j & 1) ? w[j >> 1] & 0xFFFF0000u : w[j >> 1] << 16);
+  }
+};
+
+// From element i on of a tensor of n; what is beyond reads as 0.
+template <typename T>
+__device__ __forceinline__ Four<T> load4(const T* a, int64_t i, int64_t n, bool vec) {
+  Four<T> x;
   if (vec && i + 4 <= n) {
     if constexpr (sizeof(T) == 4) {
-      const float4 u = *reinterpret_cast<const float4*>(a + i);
-      x[0] = u.x; x[1] = u.y; x[2] = u.z; x[3] = u.w;
+      const uint4 u = *reinterpret_cast<const uint4*>(a + i);
+      x.w[0] = u.x; x.w[1] = u.y; x.w[2] = u.z; x.w[3] = u.w;
     } else {
       const uint2 u = *reinterpret_cast<const uint2*>(a + i);
-      x[0] = __uint_as_float(u.x << 16); x[1] = __uint_as_float(u.x & 0xFFFF0000u);
-      x[2] = __uint_as_float(u.y << 16); x[3] = __uint_as_float(u.y & 0xFFFF0000u);
+      x.w[0] = u.x; x.w[1] = u.y;
     }
-  } else {
+  } else if constexpr (sizeof(T) == 4) {
 #pragma unroll
-    for (int j = 0; j < 4; ++j) x[j] = i + j < n ? (float)a[i + j] : 0.0f;
+    for (int j = 0; j < 4; ++j) x.w[j] = i + j < n ? __float_as_uint(a[i + j]) : 0u;
+  } else {
+    const uint16_t* h = reinterpret_cast<const uint16_t*>(a);
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+      x.w[j] = (i + 2 * j < n ? (uint32_t)h[i + 2 * j] : 0u) | (i + 2 * j + 1 < n ? (uint32_t)h[i + 2 * j + 1] << 16 : 0u);
   }
+  return x;
 }
 
 __device__ __forceinline__ void store4(float* a, int64_t i, int64_t n, bool vec, const float (&x)[4]) {
@@ -244,17 +275,19 @@ __device__ __noinline__ uint32_t exact_fields(uint32_t cm, uint32_t cv, int old_
 __device__ __forceinline__ int block_top(int field) { return min(max(field - 1023, -111), 127); }
 
 // ---- the same in fp32 with a bound on the error -----------------------------------
-// Where both ends of an interval that holds the fp64 value round to the same code, that is the
-// code; elsewhere (one element in 10^5 of an fp32 gradient) the fp64 route decides.  In fp64
-// throughout a step of 71 M elements took 611 us.
-// A magnitude is scaled so that the lowest normal octave of the codes is fp32's own: its bits
-// count the codes in steps of 2^20, gradual underflow included; a unit more or less covers the
-// rounding there.  What an addition to the bits has to carry to round up:
-//   stochastic: (field + 1/2) 2^-16 of a step; nearest: half a step, less a unit unless the code is odd.
+// In fp64 throughout a step of 71 M elements took 611 us.  Instead the moments are taken in fp32,
+// the first from two-word coefficients and an exact sum, so that both lie within three units of
+// their last place of the fp64 values; where a border between codes is that near (one element
+// in 10^5 of an fp32 gradient; a bf16 one meets borders exactly, one in 300) the fp64 route
+// decides.
+//   A magnitude is scaled so that the lowest normal octave of the codes is fp32's own: its bits
+// count the codes in steps of 2^20, gradual underflow included, and what is added to round up is
+// (field + 1/2) 2^-16 of a step, or to nearest half a step, less a unit unless the code is odd.
 template <bool SR>
-__device__ __forceinline__ uint32_t carry_of(uint32_t field16, uint32_t bits) {
-  return SR ? field16 << 4 | 8u : 0x7FFFFu + ((bits >> 20) & 1u);
+__device__ __forceinline__ uint32_t rounded(uint32_t bits, uint32_t field4) {   // field4 = 16 field
+  return SR ? bits + field4 + 8u : bits + 0x7FFFFu + ((bits >> 20) & 1u);
 }
+constexpr uint32_t kNear = 4;   // units
 
 // One state block of 128 elements in a warp, four to a lane.
 struct Block4 {
@@ -262,6 +295,10 @@ struct Block4 {
   uint32_t cm, cv;
   int tm, tv;      // exponent bytes - 127
 };
+
+__device__ __forceinline__ uint32_t pack4(const uint32_t (&c)[4]) {
+  return __byte_perm(__byte_perm(c[0], c[1], 0x0040), __byte_perm(c[2], c[3], 0x0040), 0x5410);
+}
 
 // Steps the block's parameters in place and gives its new codes and exponents.  Returns whether a
 // gradient of the lane is not finite.
@@ -271,40 +308,47 @@ __device__ __forceinline__ bool step_block(Block4& x, const Step& s, double b1, 
   // block's sums stay normal.
   const bool usual = x.tm <= 14 && x.tv <= 30;
   const float dm = power2f(min(x.tm, 14) + 112), dv = power2f(min(x.tv, 30) + 96);
-  float ym[4], em[4], yv[4];
-  float hm = 0.0f, lm = 0.0f, hv = 0.0f, z = 0.0f;
+  float ym[4], yv[4];
+  float hm = 0.0f, hv = 0.0f, z = 0.0f;
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
     const uint32_t mag = (j < 3 ? x.cm << (20 - 8 * j) : x.cm >> 4) & 0x07F00000u, neg = (x.cm << (24 - 8 * j)) & 0x80000000u;
     const uint32_t vbits = (j < 3 ? x.cv << (20 - 8 * j) : x.cv >> 4) & 0x0FF00000u;
-    const float om = __uint_as_float(__float_as_uint(__uint_as_float(mag) * dm) | neg);
-    const float sg = s.a1 * x.g[j];
-    z = fmaf(x.g[j], 0.0f, z);                       // NaN if any is not finite
-    ym[j] = fmaf(s.b1, om, sg);
-    // 5 2^-24 of the terms: a coefficient's rounding, the product's, the sum's, and those here
-    em[j] = fmaf(s.b1, fabsf(om), fabsf(sg)) * 2.9802322e-7f;
-    // four roundings of 2^-24 or less: 2 units of yv's last place, taken as 4
-    yv[j] = fmaf(s.b2, __uint_as_float(vbits) * dv, s.a2 * (x.g[j] * x.g[j]));
-    if (!usual) {
+    const float g = x.g[j], om = __uint_as_float(mag | neg) * dm;
+    z = fmaf(g, 0.0f, z);                            // NaN if any is not finite
+    // b1 m: exact for the upper 20 bits of b1 (m has four); (1 - b1) g: product and remainder
+    const float old = s.b1 * om, add = s.a1 * g;
+    float rest = fmaf(s.a1, g, -add);
+    rest = fmaf(s.a1_low, g, rest);
+    rest = fmaf(s.b1_low, om, rest);
+    const float sum = __fadd_rn(old, add), part = __fsub_rn(sum, old);
+    rest += __fadd_rn(__fsub_rn(old, __fsub_rn(sum, part)), __fsub_rn(add, part));   // what the sum dropped
+    ym[j] = sum + rest;
+    yv[j] = fmaf(s.b2, __uint_as_float(vbits) * dv, s.a2 * (g * g));   // four roundings: two units
+  }
+  if (!usual) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
       const float2 y = exact_moments((x.cm >> (8 * j)) & 255u, (x.cv >> (8 * j)) & 255u, x.tm, x.tv, x.g[j], b1, b2);
       ym[j] = y.x;
       yv[j] = y.y;
     }
-    hm = fmaxf(hm, fabsf(ym[j]) + em[j]);
-    lm = fmaxf(lm, fabsf(ym[j]) - em[j]);
+  }
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    hm = fmaxf(hm, fabsf(ym[j]));
     hv = fmaxf(hv, yv[j]);
     x.p[j] = stepped(x.p[j], ym[j], yv[j], s);
   }
-  // the block's exponents, if both ends agree on them (bits of positive floats order like them)
-  const uint32_t top_m = __reduce_max_sync(0xffffffffu, __float_as_uint(hm)), low_m = __reduce_max_sync(0xffffffffu, __float_as_uint(lm));
-  const uint32_t top_v = __reduce_max_sync(0xffffffffu, __float_as_uint(hv));
+  // the block's exponents (bits of positive floats order like them), open next to a power of two
+  const uint32_t top_m = __reduce_max_sync(0xffffffffu, __float_as_uint(hm)), top_v = __reduce_max_sync(0xffffffffu, __float_as_uint(hv));
   int tm = (int)(top_m >> 23) - 127, tv = (int)(top_v >> 23) - 127;
-  const uint32_t edge = ((top_v & 0x7FFFFFu) + 8u) & 0x7FFFFFu;   // below 16: within 8 units of a power of two
+  const uint32_t edge = min((top_m + kNear) & 0x7FFFFFu, (top_v + kNear) & 0x7FFFFFu);
   const bool odd = z != z;
-  const bool open = !usual || __any_sync(0xffffffffu, odd) || ((top_m ^ low_m) >> 23) != 0u || tm > 14 || tm < -60 || tv > 30 ||
-                    tv < -60 || edge < 16u;
-  uint32_t om = 0, ov = 0, redo = 0;
+  const bool open = !usual || __any_sync(0xffffffffu, odd) || tm > 14 || tm < -60 || tv > 30 || tv < -60 || edge <= 2 * kNear;
+  uint32_t om, ov, redo = 0;
   if (open) {
+    om = ov = 0;
     const bool some = (x.cm | x.cv) != 0u || x.g[0] != 0.0f || x.g[1] != 0.0f || x.g[2] != 0.0f || x.g[3] != 0.0f;
     if (!__any_sync(0xffffffffu, some)) {   // nothing there, and nothing new
       tm = tv = -111;
@@ -321,25 +365,33 @@ __device__ __forceinline__ bool step_block(Block4& x, const Step& s, double b1, 
     }
   } else {
     const float sm = power2f(-112 - tm), sv = power2f(-96 - tv);
-    uint32_t cm[4], cv[4];
+    uint32_t rm[4], rv[4], cm[4], cv[4], near = 0xFFFFFu;
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      const float a = fabsf(ym[j]);
-      const uint32_t bh = __float_as_uint((a + em[j]) * sm), bl = __float_as_uint(fmaxf(a - em[j], 0.0f) * sm);
-      const uint32_t high = bh + carry_of<SR>(w.w[j] & 0xFFFFu, bh) + 1u, low = bl + carry_of<SR>(w.w[j] & 0xFFFFu, bl) - 1u;
-      const uint32_t bv = __float_as_uint(yv[j] * sv);
-      const uint32_t carry = carry_of<SR>(w.w[j] >> 16, bv);
-      // the low end of v: its own carry would differ from this one only across a code's border,
-      // and then the codes differ
-      const uint32_t vh = bv + carry + 4u, vl = bv + carry - 4u;
-      if (((high ^ low) | (vh ^ vl)) >> 20) redo |= 1u << j;
-      if (yv[j] == 0.0f && (x.g[j] != 0.0f || (x.cv >> (8 * j)) & 255u)) redo |= 1u << j;   // fp64 may see more
-      cm[j] = min(high >> 20, 127u);
-      cm[j] |= cm[j] ? (__float_as_uint(ym[j]) >> 24) & 128u : 0u;
-      cv[j] = max(min(vh >> 20, 255u), min(__float_as_uint(yv[j]), 1u));
+      rm[j] = rounded<SR>(__float_as_uint(fabsf(ym[j]) * sm), (w.w[j] << 4) & 0xFFFF0u);
+      rv[j] = rounded<SR>(__float_as_uint(yv[j] * sv), (w.w[j] >> 12) & 0xFFFF0u);
+      near = min(near, min((rm[j] + kNear) & 0xFFFFFu, (rv[j] + kNear) & 0xFFFFFu));
+      cm[j] = rm[j] >> 20;
+      cv[j] = min(rv[j] >> 20, 255u);
     }
-    om = __byte_perm(__byte_perm(cm[0], cm[1], 0x0040), __byte_perm(cm[2], cm[3], 0x0040), 0x5410);
-    ov = __byte_perm(__byte_perm(cv[0], cv[1], 0x0040), __byte_perm(cv[2], cv[3], 0x0040), 0x5410);
+    om = pack4(cm);
+    om -= (om & 0x80808080u) >> 7;                   // 128, past the top code, becomes 127
+    const uint32_t b[4] = {__float_as_uint(ym[0]) >> 24, __float_as_uint(ym[1]) >> 24, __float_as_uint(ym[2]) >> 24, __float_as_uint(ym[3]) >> 24};
+    om |= (om + 0x7F7F7F7Fu) & pack4(b) & 0x80808080u;   // signs of codes that are not zero
+    ov = pack4(cv);
+    if (near <= 2 * kNear) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        if (min((rm[j] + kNear) & 0xFFFFFu, (rv[j] + kNear) & 0xFFFFFu) <= 2 * kNear) redo |= 1u << j;
+    }
+    if ((ov - 0x01010101u) & ~ov & 0x80808080u) {    // a zero code of v: 1 where v is positive
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        if (!((ov >> (8 * j)) & 255u)) {
+          if (yv[j] > 0.0f) ov |= 1u << (8 * j);
+          else if (x.g[j] != 0.0f || (x.cv >> (8 * j)) & 255u) redo |= 1u << j;   // fp64 may see more
+        }
+    }
   }
   while (redo) {
     const int j = __ffs(redo) - 1;
@@ -367,10 +419,8 @@ struct View {
   int64_t n;
   bool vec_p, vec_g, vec_s;
   __device__ __forceinline__ bool in(int64_t i) const { return FAST || i < n; }
-  __device__ __forceinline__ void load(int64_t i, float (&xp)[4], float (&xg)[4]) const {
-    load4(p, i, FAST ? i + 4 : n, FAST || vec_p, xp);
-    load4(g, i, FAST ? i + 4 : n, FAST || vec_g, xg);
-  }
+  __device__ __forceinline__ Four<T> load_p(int64_t i) const { return load4(p, i, FAST ? i + 4 : n, FAST || vec_p); }
+  __device__ __forceinline__ Four<T> load_g(int64_t i) const { return load4(g, i, FAST ? i + 4 : n, FAST || vec_g); }
   __device__ __forceinline__ void store(int64_t i, const float (&xp)[4], bool sr, const Words4& w) const {
     if constexpr (sizeof(T) == 4) store4(p, i, FAST ? i + 4 : n, FAST || vec_p, xp);
     else store4(p, i, FAST ? i + 4 : n, FAST || vec_p, xp, sr, w);
@@ -390,16 +440,16 @@ __device__ __forceinline__ bool run_chunk(const Table<CAP>& tab, int which, int6
 #pragma unroll 2
     for (int u = 0; u < tab.units; ++u, i += kUnit) {
       if (!a.in(i)) break;
-      float xp[4], xg[4], xm[4], xv[4], z = 0.0f;
-      a.load(i, xp, xg);
-      load4(m, i, FAST ? i + 4 : a.n, FAST || a.vec_s, xm);
-      load4(v, i, FAST ? i + 4 : a.n, FAST || a.vec_s, xv);
+      const Four<T> fp = a.load_p(i), fg = a.load_g(i);
+      const Four<float> fm = load4(m, i, FAST ? i + 4 : a.n, FAST || a.vec_s), fv = load4(v, i, FAST ? i + 4 : a.n, FAST || a.vec_s);
+      float xp[4], xm[4], xv[4], z = 0.0f;
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        z = fmaf(xg[j], 0.0f, z);
-        xm[j] = fmaf(s.b1, xm[j], s.a1 * xg[j]);
-        xv[j] = fmaf(s.b2, xv[j], s.a2 * (xg[j] * xg[j]));
-        xp[j] = stepped(xp[j], xm[j], xv[j], s);
+        const float g = fg.get(j), old = fm.get(j);
+        z = fmaf(g, 0.0f, z);
+        xm[j] = fmaf(s.b1, old, fmaf(s.b1_low, old, s.a1 * g));
+        xv[j] = fmaf(s.b2, fv.get(j), s.a2 * (g * g));
+        xp[j] = stepped(fp.get(j), xm[j], xv[j], s);
       }
       bad |= z != z;
       store4(m, i, FAST ? i + 4 : a.n, FAST || a.vec_s, xm);
@@ -413,35 +463,56 @@ __device__ __forceinline__ bool run_chunk(const Table<CAP>& tab, int which, int6
     uint8_t* v = static_cast<uint8_t*>(a.v);
     uint8_t* me = tab.t[which].me;
     uint8_t* ve = tab.t[which].ve;
+    // A warp takes `units` consecutive state blocks; their exponents are read and written at once, a
+    // lane each.  (One at a time, stored beside others still to be read, they cost more than
+    // all the rest: 71 M elements 466 us, 220 without them.)
     const int lane = threadIdx.x & 31;
-    int64_t i = base + (int64_t)threadIdx.x * 4;   // a warp takes one state block of each unit
-    auto load = [&](int64_t i, Block4& x) {
-      a.load(i, x.p, x.g);
-      x.cm = load_codes(m, i, FAST ? i + 4 : a.n, FAST || a.vec_s);
-      x.cv = load_codes(v, i, FAST ? i + 4 : a.n, FAST || a.vec_s);
-      const int64_t blk = i / kStateBlock;
-      x.tm = (int)me[blk] - 127;
-      x.tv = (int)ve[blk] - 127;
+    const int64_t first = base + (int64_t)(threadIdx.x >> 5) * tab.units * kStateBlock;
+    if (!a.in(first)) return false;
+    const int blocks = FAST ? tab.units : (int)min((int64_t)tab.units, (a.n - first + kStateBlock - 1) / kStateBlock);
+    const int64_t blk = first / kStateBlock + lane;
+    const int old_me = lane < blocks ? (int)me[blk] - 127 : 0, old_ve = lane < blocks ? (int)ve[blk] - 127 : 0;
+    int new_me = 0, new_ve = 0;
+    int64_t i = first + lane * 4;
+    struct {
+      Four<T> p, g;
+      uint32_t cm, cv;
+    } next;
+    auto load = [&](int64_t i) {
+      next.p = a.load_p(i);
+      next.g = a.load_g(i);
+      next.cm = load_codes(m, i, FAST ? i + 4 : a.n, FAST || a.vec_s);
+      next.cv = load_codes(v, i, FAST ? i + 4 : a.n, FAST || a.vec_s);
     };
-    const int64_t first = i - lane * 4;            // of the warp's block
-    Block4 next;
-    if (a.in(first)) load(i, next);
-    for (int u = 0; u < tab.units; ++u, i += kUnit) {
-      if (!a.in(i - lane * 4)) break;
-      Block4 x = next;
-      if (u + 1 < tab.units && a.in(i - lane * 4 + kUnit)) load(i + kUnit, next);
+    load(i);
+    for (int u = 0; u < blocks; ++u, i += kStateBlock) {
+      Block4 x;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        x.p[j] = next.p.get(j);
+        x.g[j] = next.g.get(j);
+      }
+      x.cm = next.cm;
+      x.cv = next.cv;
+      x.tm = __shfl_sync(0xffffffffu, old_me, u);
+      x.tv = __shfl_sync(0xffffffffu, old_ve, u);
+      if (u + 1 < blocks) load(i + kStateBlock);
       Words4 w{};
       if (SR) w = stream_words(tab.keys, tag, s.t, (uint64_t)i >> 2);
       bad |= step_block<SR>(x, s, tab.c.b1, tab.c.b2, w);
       store_codes(m, i, FAST ? i + 4 : a.n, FAST || a.vec_s, x.cm);
       store_codes(v, i, FAST ? i + 4 : a.n, FAST || a.vec_s, x.cv);
-      if (lane == 0) {
-        me[i / kStateBlock] = (uint8_t)(x.tm + 127);
-        ve[i / kStateBlock] = (uint8_t)(x.tv + 127);
+      if (lane == u) {
+        new_me = x.tm + 127;
+        new_ve = x.tv + 127;
       }
       Words4 wp{};
       if (SR && sizeof(T) == 2) wp = stream_words(tab.keys, tag | 1u, s.t, (uint64_t)i >> 2);
       a.store(i, x.p, SR, wp);
+    }
+    if (lane < blocks) {
+      me[blk] = (uint8_t)new_me;
+      ve[blk] = (uint8_t)new_ve;
     }
   }
   return bad;
