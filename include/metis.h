@@ -386,6 +386,31 @@ metis_status metis_gemm_int8(metis_ctx* ctx, const metis_int8* A, const metis_in
 metis_status metis_linear_int8(metis_ctx* ctx, const void* X, int64_t ld, int32_t dtype, metis_int8* Xq,
                                const metis_int8* W, void* C, int64_t ldc, int32_t c_dtype);
 
+/* Dense device matrix of either type, row-major with leading dimension ld >= cols (elements). */
+typedef struct {
+  const void* data;
+  int64_t rows, cols, ld;
+  int32_t dtype;             /* METIS_OUT_* */
+} metis_dense;
+
+/*
+ * Training layer Y = X W on 8-bit operands (X: l x m, W: m x n), each quantized along the
+ * dimension that its product contracts:
+ * metis_int8_linear_fwd: Xrow <- Q(X) by tokens (l x m), Wcol <- Q(W) by output channels
+ *   (n x m, needs scratch), Y = Xrow Wcol^T (l x n).  For a backward pass also, each nullable:
+ *   Xcol <- Q(X) by input channels (m x l, needs scratch), Wrow <- Q(W) by input channels (m x n).
+ * metis_int8_linear_bwd: D (l x n) is quantized as the products asked for need it:
+ *   dX (nullable) = Drow Wrow^T (l x m, type dx_dtype), Drow <- Q(D) by tokens (l x n);
+ *   dW (nullable) = Xcol Dcol^T (m x n fp32), Dcol <- Q(D) by output channels (n x l, needs scratch).
+ * The same results as the calls above one by one.  l, m, n <= 131071 where they are contracted.
+ */
+metis_status metis_int8_linear_fwd(metis_ctx* ctx, const metis_dense* X, const metis_dense* W, metis_int8* Xrow,
+                                   metis_int8* Xcol, metis_int8* Wrow, metis_int8* Wcol, void* Y, int64_t ldy,
+                                   int32_t y_dtype);
+metis_status metis_int8_linear_bwd(metis_ctx* ctx, const metis_dense* D, metis_int8* Drow, metis_int8* Dcol,
+                                   const metis_int8* Xcol, const metis_int8* Wrow, void* dX, int64_t lddx,
+                                   int32_t dx_dtype, float* dW, int64_t lddw);
+
 /*
  * One AdamW step over many tensors:
  *   m = b1 m + (1 - b1) g,   v = b2 v + (1 - b2) g^2,

@@ -48,7 +48,7 @@ EXPORTED = ["metis_create", "metis_destroy", "metis_set_stream", "metis_status_s
             "metis_lora_branch_grad", "metis_lora_constrain", "metis_lora_realign",
             "metis_residual_quantize_nvfp4_dump", "metis_profile_read_kind", "metis_set_sm_count_target",
             "metis_selftest_numeric", "metis_quantize_int8", "metis_gemm_int8", "metis_linear_int8",
-            "metis_adamw_step"]
+            "metis_adamw_step", "metis_int8_linear_fwd", "metis_int8_linear_bwd"]
 
 PROF_GEMM, PROF_RESQUANT, PROF_PROJECTION = 0, 1, 2
 
@@ -79,6 +79,10 @@ class QuantParams(ctypes.Structure):
 class Int8Struct(ctypes.Structure):
     _fields_ = [("codes", c_p), ("scales", c_p), ("outer", c_i64), ("inner", c_i64), ("ld", c_i64),
                 ("scratch", c_p)]
+
+
+class Dense(ctypes.Structure):
+    _fields_ = [("data", c_p), ("rows", c_i64), ("cols", c_i64), ("ld", c_i64), ("dtype", c_i32)]
 
 
 class AdamWTensor(ctypes.Structure):
@@ -146,6 +150,11 @@ _quant_i8 = _sig("metis_quantize_int8", c_i32, c_p, c_p, c_i64, c_i64, c_i64, c_
 _gemm_i8 = _sig("metis_gemm_int8", c_i32, c_p, ctypes.POINTER(Int8Struct), ctypes.POINTER(Int8Struct), c_p, c_i64, c_i32)
 _linear_i8 = _sig("metis_linear_int8", c_i32, c_p, c_p, c_i64, c_i32, ctypes.POINTER(Int8Struct),
                   ctypes.POINTER(Int8Struct), c_p, c_i64, c_i32)
+_int8_p, _dense_p = ctypes.POINTER(Int8Struct), ctypes.POINTER(Dense)
+_int8_fwd = _sig("metis_int8_linear_fwd", c_i32, c_p, _dense_p, _dense_p, _int8_p, _int8_p, _int8_p, _int8_p, c_p, c_i64,
+                 c_i32)
+_int8_bwd = _sig("metis_int8_linear_bwd", c_i32, c_p, _dense_p, _int8_p, _int8_p, _int8_p, _int8_p, c_p, c_i64, c_i32, c_p,
+                 c_i64)
 _adamw = _sig("metis_adamw_step", c_i32, c_p, c_p, c_i64, ctypes.POINTER(AdamWParams))
 
 _launches = _sig("metis_kernel_launches", c_u64)
@@ -169,6 +178,11 @@ class MetisError(RuntimeError):
 
 def status_str(status):
     return _status_str(status).decode()
+
+
+# The current stream's handle, without the Stream object around it.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+    (lambda index: torch.cuda.current_stream(index).cuda_stream)
 
 
 def _ptr(t):
@@ -291,7 +305,7 @@ class Context:
             pass
 
     def _call(self, fn, *args):
-        _set_stream(self._h, c_p(torch.cuda.current_stream(self.device).cuda_stream))
+        _set_stream(self._h, _raw_stream(self.device.index))
         st = fn(self._h, *args)
         if st != METIS_OK:
             raise MetisError(st, _last_error(self._h).decode())
@@ -453,6 +467,31 @@ class Context:
         if X.shape != (Xq.outer, Xq.inner) or Y.shape != (Xq.outer, W.outer):
             raise ValueError("expected X like Xq (tokens x in) and Y of tokens x out")
         self._call(_linear_i8, ptr, ld, dtype, ctypes.byref(Xq.struct), ctypes.byref(W.struct), yptr, ldy, ydtype)
+
+    def int8_linear_fwd(self, X, W, Y, Xrow, Wcol, Xcol=None, Wrow=None):
+        """Training forward pass Y = Q(X) Q(W): the operands are Int8Struct of the layer's buffers."""
+        self._same_device(X=X, W=W, Y=Y)
+        x, w, (ptr, ldy, dtype) = self._dense_struct(X, "X"), self._dense_struct(W, "W"), _dense(Y, "Y")
+        if Y.shape != (X.shape[0], W.shape[1]):
+            raise ValueError("expected Y of X's rows and W's columns")
+        self._call(_int8_fwd, x, w, Xrow, Xcol, Wrow, Wcol, ptr, ldy, dtype)
+
+    def int8_linear_bwd(self, D, Drow=None, Dcol=None, Xcol=None, Wrow=None, dX=None, dW=None):
+        """Training backward pass: dX = Q(D) Q(W)^T and / or dW = Q(X)^T Q(D) (fp32)."""
+        self._same_device(D=D, dX=dX, dW=dW)
+        xptr, ldx, xdtype = (None, 0, OUT_F32) if dX is None else _dense(dX, "dX")
+        wptr, ldw, wdtype = (None, 0, OUT_F32) if dW is None else _dense(dW, "dW")
+        if wdtype != OUT_F32:
+            raise ValueError("dW: expected fp32")
+        if (dX is not None and Wrow is not None and dX.shape != (D.shape[0], Wrow.outer)) or \
+                (dW is not None and Xcol is not None and dW.shape != (Xcol.outer, D.shape[1])):
+            raise ValueError("dX or dW of another shape than its operands'")
+        self._call(_int8_bwd, self._dense_struct(D, "D"), Drow, Dcol, Xcol, Wrow, xptr, ldx, xdtype, wptr, ldw)
+
+    @staticmethod
+    def _dense_struct(M, name):
+        ptr, ld, dtype = _dense(M, name)
+        return Dense(ptr, M.shape[0], M.shape[1], ld, dtype)
 
     # -- optimizer step -----------------------------------------------------------
     def adamw_step(self, tensors, count, lr, beta1, beta2, eps, weight_decay, step, state_bits=32, rounding=0, seed=0,

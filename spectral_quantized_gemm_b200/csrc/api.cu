@@ -650,6 +650,12 @@ metis_status check_gemm_int8(metis_ctx* ctx, const metis_int8* A, const metis_in
   return METIS_OK;
 }
 
+metis_status quantize_int8(metis_ctx* ctx, const metis_dense* M, const metis_int8* row, const metis_int8* col) {
+  return check_cuda(ctx, launch_quantize_i8(M->data, M->dtype == METIS_OUT_BF16, M->rows, M->cols, M->ld, row, col,
+                                            ctx->status, ctx->sm_count, ctx->stream),
+                    "int8 quantize launch");
+}
+
 metis_status check_adamw(metis_ctx* ctx, const metis_adamw_tensor* tensors, int64_t count, const metis_adamw_params* q) {
   if (!q || count < 0 || (count > 0 && !tensors)) return fail(ctx, METIS_ERR_ARG, "null parameters or tensors");
   if (q->state_bits != 8 && q->state_bits != 32) return fail(ctx, METIS_ERR_ARG, "state_bits must be 8 or 32");
@@ -689,9 +695,8 @@ metis_status metis_quantize_int8(metis_ctx* ctx, const void* M, int64_t rows, in
   return guarded(ctx, [&] {
     const metis_status s = check_quantize_int8(ctx, M, rows, cols, ld, dtype, rowwise, colwise);
     if (s != METIS_OK) return s;
-    return check_cuda(ctx, launch_quantize_i8(M, dtype == METIS_OUT_BF16, rows, cols, ld, rowwise, colwise, ctx->status,
-                                              ctx->sm_count, ctx->stream),
-                      "int8 quantize launch");
+    const metis_dense dense{M, rows, cols, ld, dtype};
+    return quantize_int8(ctx, &dense, rowwise, colwise);
   });
 }
 
@@ -711,10 +716,43 @@ metis_status metis_linear_int8(metis_ctx* ctx, const void* X, int64_t ld, int32_
     if (!Xq) return fail(ctx, METIS_ERR_ARG, "null operand");
     metis_status s = check_quantize_int8(ctx, X, Xq->outer, Xq->inner, ld, dtype, Xq, nullptr);
     if (s != METIS_OK || (s = check_gemm_int8(ctx, Xq, W, C, ldc, c_dtype)) != METIS_OK) return s;
-    s = check_cuda(ctx, launch_quantize_i8(X, dtype == METIS_OUT_BF16, Xq->outer, Xq->inner, ld, Xq, nullptr,
-                                           ctx->status, ctx->sm_count, ctx->stream),
-                   "int8 quantize launch");
+    const metis_dense dense{X, Xq->outer, Xq->inner, ld, dtype};
+    s = quantize_int8(ctx, &dense, Xq, nullptr);
     return s == METIS_OK ? launch_gemm_i8(ctx, Xq, W, C, ldc, c_dtype, true) : s;
+  });
+}
+
+metis_status metis_int8_linear_fwd(metis_ctx* ctx, const metis_dense* X, const metis_dense* W, metis_int8* Xrow,
+                                   metis_int8* Xcol, metis_int8* Wrow, metis_int8* Wcol, void* Y, int64_t ldy,
+                                   int32_t y_dtype) {
+  const metis::NvtxRange nvtx_range("metis_int8_linear_fwd");
+  return guarded(ctx, [&] {
+    if (!X || !W || !Xrow || !Wcol) return fail(ctx, METIS_ERR_ARG, "null operand");
+    if (X->cols != W->rows) return fail(ctx, METIS_ERR_SHAPE, "X.cols must equal W.rows");
+    metis_status s = check_quantize_int8(ctx, X->data, X->rows, X->cols, X->ld, X->dtype, Xrow, Xcol);
+    if (s != METIS_OK || (s = check_quantize_int8(ctx, W->data, W->rows, W->cols, W->ld, W->dtype, Wrow, Wcol)) != METIS_OK ||
+        (s = check_gemm_int8(ctx, Xrow, Wcol, Y, ldy, y_dtype)) != METIS_OK)
+      return s;
+    if ((s = quantize_int8(ctx, X, Xrow, Xcol)) != METIS_OK || (s = quantize_int8(ctx, W, Wrow, Wcol)) != METIS_OK) return s;
+    return launch_gemm_i8(ctx, Xrow, Wcol, Y, ldy, y_dtype, false);
+  });
+}
+
+metis_status metis_int8_linear_bwd(metis_ctx* ctx, const metis_dense* D, metis_int8* Drow, metis_int8* Dcol,
+                                   const metis_int8* Xcol, const metis_int8* Wrow, void* dX, int64_t lddx,
+                                   int32_t dx_dtype, float* dW, int64_t lddw) {
+  const metis::NvtxRange nvtx_range("metis_int8_linear_bwd");
+  return guarded(ctx, [&] {
+    if (!D || (!dX && !dW) || (dX && (!Drow || !Wrow)) || (dW && (!Dcol || !Xcol)))
+      return fail(ctx, METIS_ERR_ARG, "null operand");
+    metis_int8 *row = dX ? Drow : nullptr, *col = dW ? Dcol : nullptr;
+    metis_status s = check_quantize_int8(ctx, D->data, D->rows, D->cols, D->ld, D->dtype, row, col);
+    if (s != METIS_OK || (dX && (s = check_gemm_int8(ctx, Drow, Wrow, dX, lddx, dx_dtype)) != METIS_OK) ||
+        (dW && (s = check_gemm_int8(ctx, Xcol, Dcol, dW, lddw, METIS_OUT_F32)) != METIS_OK))
+      return s;
+    if ((s = quantize_int8(ctx, D, row, col)) != METIS_OK) return s;
+    if (dX && (s = launch_gemm_i8(ctx, Drow, Wrow, dX, lddx, dx_dtype, false)) != METIS_OK) return s;
+    return dW ? launch_gemm_i8(ctx, Xcol, Dcol, dW, lddw, METIS_OUT_F32, false) : METIS_OK;
   });
 }
 

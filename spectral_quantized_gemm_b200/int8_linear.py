@@ -25,7 +25,7 @@ import math
 
 import torch
 
-from . import Int8
+from . import INT8_SCRATCH, Int8Struct
 from .linear import _shared_context
 
 MAX_INNER = 131071
@@ -44,6 +44,25 @@ def _operand(M):
     return M if M.stride(-1) == 1 or M.shape[-1] == 1 else M.contiguous()
 
 
+def _buffers(device, *sizes):
+    """One allocation for the operands of sizes (outer, inner, columns): their Int8Struct and the
+    tensor that holds them.  columns: quantized column-wise, so with the scratch for it."""
+    at, places = 0, []
+    for outer, inner, columns in sizes:
+        ld = -(-inner // 16) * 16
+        scales = at + outer * ld
+        places.append((at, scales, scales + 4 * outer, ld))
+        at = -(-(scales + 4 * outer * (1 + (INT8_SCRATCH if columns else 0))) // 256) * 256
+    buf = torch.empty(at, dtype=torch.uint8, device=device)
+    return buf, _views(buf, sizes, places)
+
+
+def _views(buf, sizes, places):
+    base = buf.data_ptr()
+    return [Int8Struct(base + codes, base + scales, outer, inner, ld, base + scratch if columns else None)
+            for (outer, inner, columns), (codes, scales, scratch, ld) in zip(sizes, places)]
+
+
 class _Int8LinearFn(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, weight):
@@ -53,15 +72,17 @@ class _Int8LinearFn(torch.autograd.Function):
         if rows == 0:
             return torch.empty(0, n, dtype=torch.bfloat16, device=x.device)
         x, w = _operand(x), _operand(weight)
+        # what the backward pass reads is kept, the rest goes with this call
+        kept_sizes = ([(m, rows, True)] if need_dw else []) + ([(m, n, False)] if need_dx else [])
+        kept, saved = _buffers(x.device, *kept_sizes) if kept_sizes else (None, [])
+        work, (xr, wc) = _buffers(x.device, (rows, m, False), (n, m, True))
+        y = _output(rows, n, torch.bfloat16, x.device)
         lib, lock = _shared_context(x.device)
         with lock:
-            xr, xc = lib.new_int8(rows, m), lib.new_int8(m, rows) if need_dw else None
-            wr, wc = lib.new_int8(m, n) if need_dx else None, lib.new_int8(n, m)
-            lib.quantize_int8(x, rowwise=xr, colwise=xc)
-            lib.quantize_int8(w, rowwise=wr, colwise=wc)
-            y = _output(rows, n, torch.bfloat16, x.device)
-            lib.gemm_int8(xr, wc, y)
-        ctx.save_for_backward(*(t for q in (xc, wr) if q is not None for t in (q.codes, q.scales)))
+            lib.int8_linear_fwd(x, w, y, xr, wc, Xcol=saved[0] if need_dw else None, Wrow=saved[-1] if need_dx else None)
+        if kept is not None:
+            ctx.save_for_backward(kept)
+            ctx.kept = [(s.outer, s.inner, s.ld, s.codes - kept.data_ptr(), s.scales - kept.data_ptr()) for s in saved]
         return y
 
     @staticmethod
@@ -72,22 +93,17 @@ class _Int8LinearFn(torch.autograd.Function):
         if rows == 0:
             return (torch.empty(0, m, dtype=ctx.x_dtype, device=dy.device) if need_dx else None,
                     torch.zeros(m, n, dtype=ctx.w_dtype, device=dy.device) if need_dw else None)
-        saved = list(ctx.saved_tensors)
+        kept, = ctx.saved_tensors
+        base = kept.data_ptr()
+        saved = [Int8Struct(base + codes, base + scales, outer, inner, ld, None) for outer, inner, ld, codes, scales in ctx.kept]
         dy = _operand(dy)
+        work, new = _buffers(dy.device, *([(n, rows, True)] if need_dw else []), *([(rows, n, False)] if need_dx else []))
+        dx = _output(rows, m, torch.bfloat16 if ctx.x_dtype == torch.bfloat16 else torch.float32, dy.device) if need_dx else None
+        dw = _output(m, n, torch.float32, dy.device) if need_dw else None
         lib, lock = _shared_context(dy.device)
-        dx = dw = None
         with lock:
-            dr = lib.new_int8(rows, n) if need_dx else None
-            dc = lib.new_int8(n, rows) if need_dw else None
-            lib.quantize_int8(dy, rowwise=dr, colwise=dc)
-            if need_dw:
-                xc = Int8(m, rows, codes=saved[0], scales=saved[1])
-                dw = _output(m, n, torch.float32, dy.device)
-                lib.gemm_int8(xc, dc, dw)
-            if need_dx:
-                wr = Int8(m, n, codes=saved[-2], scales=saved[-1])
-                dx = _output(rows, m, torch.float32 if ctx.x_dtype != torch.bfloat16 else torch.bfloat16, dy.device)
-                lib.gemm_int8(dr, wr, dx)
+            lib.int8_linear_bwd(dy, Drow=new[-1] if need_dx else None, Dcol=new[0] if need_dw else None,
+                                Xcol=saved[0] if need_dw else None, Wrow=saved[-1] if need_dx else None, dX=dx, dW=dw)
         return (dx.to(ctx.x_dtype) if need_dx else None, dw.to(ctx.w_dtype) if need_dw else None)
 
 

@@ -20,7 +20,9 @@ captured into a CUDA graph and replayed; take one step before the capture, which
 the states.  There is no CPU path.
 """
 
-import numpy as np
+import array
+import operator
+
 import torch
 
 from . import OUT_BF16, OUT_F32
@@ -28,8 +30,7 @@ from .linear import _shared_context
 
 BLOCK = 128    # elements that share an exponent of an 8-bit state
 
-_ENTRY = np.dtype([("p", "u8"), ("g", "u8"), ("m", "u8"), ("v", "u8"), ("m_exponent", "u8"), ("v_exponent", "u8"),
-                   ("n", "i8"), ("dtype", "i4"), ("id", "u4")])
+ENTRY_WORDS = 8    # 64-bit words of a metis_adamw_tensor: six addresses, n, dtype | id << 32
 
 
 def _dense_layout(t):
@@ -42,6 +43,43 @@ def _dense_layout(t):
             return False
         expected *= size
     return True
+
+
+class _Plan:
+    """The entries of a group's last step and the objects that they were made from.  The next step
+    uses them again, with the addresses of its gradients, if every object is still the same and
+    lies where it lay; anything else goes through the checks of a first step."""
+
+    def __init__(self, params, dtypes, sizes, tensors, all_states, states, entries, device):
+        self.params, self.dtypes, self.sizes, self.tensors = params, dtypes, sizes, tensors
+        self.all_states, self.states, self.entries, self.device = all_states, states, entries, device
+        self.where = self.addresses()
+
+    def addresses(self):
+        return [t.data_ptr() for t in self.tensors]
+
+    def renew(self, params, all_states, keys, t):
+        """Whether the plan holds; then its entries are those of the step t (None: not counted here)."""
+        if len(params) != len(self.params) or not all(map(operator.is_, params, self.params)) or \
+                len(all_states) != len(self.all_states) or not all(map(operator.is_, all_states.values(), self.all_states)):
+            return False
+        grads = [p.grad for p in params]
+        if any(g is None for g in grads) or [g.dtype for g in grads] != self.dtypes or \
+                [g.numel() for g in grads] != self.sizes or not all([g.is_contiguous() and g.is_cuda for g in grads]):
+            return False
+        if not all(map(operator.is_, self.tensors[len(params):], [s[k] for k in keys for s in self.states])) or \
+                self.addresses() != self.where:
+            return False
+        if t is not None:
+            if any([s["step"] != t for s in self.states]):
+                return False
+            for s in self.states:
+                s["step"] = t + 1
+        self.entries[1::ENTRY_WORDS] = array.array("Q", [g.data_ptr() for g in grads])
+        return True
+
+
+_KEYS = {32: ("exp_avg", "exp_avg_sq"), 8: ("exp_avg", "exp_avg_sq", "exp_avg_exponent", "exp_avg_sq_exponent")}
 
 
 class AdamW(torch.optim.Optimizer):
@@ -120,72 +158,120 @@ class AdamW(torch.optim.Optimizer):
         if closure is not None:
             with torch.enable_grad():
                 loss = closure()
+        plans = self.__dict__.setdefault("_plans", {})
         first = 0
-        for group in self.param_groups:
-            self._step_group(group, first)
+        for number, group in enumerate(self.param_groups):
+            plan = plans.get((number, first, group["state_bits"], group["capturable"]))
+            if plan is None or not self._step_again(group, plan):
+                plans[number, first, group["state_bits"], group["capturable"]] = self._step_group(group, first)
             first += len(group["params"])
         return loss
 
+    def __getstate__(self):
+        state = super().__getstate__()
+        state.pop("_plans", None)
+        return state
+
+    def _step_again(self, group, plan):
+        """The step from a plan that still holds; False if it does not."""
+        if torch.cuda.is_current_stream_capturing() and not group["capturable"]:
+            return False
+        t = None if group["capturable"] else plan.states[0]["step"]
+        if not plan.renew(group["params"], self.state, _KEYS[group["state_bits"]], t):
+            return False
+        if t is None:
+            group["step_count"] += 1
+        self._launch(group, plan.device, t, plan.entries)
+        return True
+
+    def _launch(self, group, device, t, rows):
+        lr, (b1, b2) = group["lr"], group["betas"]
+        on_device = isinstance(lr, torch.Tensor)
+        lib, lock = _shared_context(device)
+        with lock:
+            lib.adamw_step(rows.buffer_info()[0], len(rows) // ENTRY_WORDS, 0.0 if on_device else float(lr), b1, b2,
+                           group["eps"], group["weight_decay"], 1 if t is None else t + 1, group["state_bits"],
+                           1 if group["rounding"] == "sr" else 0, self.seed, lr_dev=lr if on_device else None,
+                           step_dev=group["step_count"] if t is None else None)
+
     def _step_group(self, group, first):
         bits, capturable = group["state_bits"], group["capturable"]
-        calls = {}      # (device, step) -> rows of entries
-        keep = []       # gradients copied into their parameter's layout
-        todo = [(i, p, p.grad) for i, p in enumerate(group["params"]) if p.grad is not None]
+        todo = [(i, p, g) for i, p in enumerate(group["params"]) if (g := p.grad) is not None]
         if not todo:
-            return
-        if not all(p.is_cuda for _, p, _ in todo):
+            return None
+        device = todo[0][1].device
+        if device.type != "cuda":
             raise ValueError("parameters must be on a CUDA device")
         capturing = torch.cuda.is_current_stream_capturing()
         if capturing and not capturable:
             raise RuntimeError("step() under capture needs capturable=True")
+        calls = {}      # (device, steps taken) -> flat list of the entries' numbers
+        keep = []       # gradients copied into their parameter's layout
+        counted = []    # (state, its next step), set once all is checked
+        state_dtype = torch.uint8 if bits == 8 else torch.float32
+        states = self.state
+        t = None
         for i, p, g in todo:
-            if g.layout != torch.strided or g.dtype != p.dtype or g.device != p.device:
-                raise ValueError("a gradient must be dense, of its parameter's type and on its device")
-            if not _dense_layout(p):
-                raise ValueError("a parameter's elements must fill one stretch of memory")
-            if g.stride() != p.stride():
-                g = torch.empty_like(p, memory_format=torch.preserve_format).copy_(g)
-                keep.append(g)
-            state = self.state[p]
+            dtype, n = p.dtype, p.numel()
+            if not (g.layout is torch.strided and g.dtype is dtype and g.numel() == n and p.device == g.device and p.is_cuda):
+                raise ValueError("a gradient must be dense, of its parameter's type and size, both on one CUDA device")
+            plain = p.is_contiguous()
+            if not (plain and g.is_contiguous()):
+                g = self._same_layout(p, g, keep)
+            state = states[p]
             if "exp_avg" not in state:
                 if capturing:
                     raise RuntimeError("take one step before the capture: it creates the states")
                 state.update(self._new_state(p, bits))
             m, v = state["exp_avg"], state["exp_avg_sq"]
-            want = torch.uint8 if bits == 8 else torch.float32
-            if m.dtype != want or v.dtype != want or m.shape != p.shape or v.shape != p.shape or \
-                    m.stride() != p.stride() or v.stride() != p.stride():
+            if not (m.dtype is state_dtype and v.dtype is state_dtype and m.numel() == n and v.numel() == n and
+                    m.is_cuda and v.is_cuda and
+                    (m.is_contiguous() and v.is_contiguous() if plain else m.stride() == p.stride() == v.stride())):
                 raise ValueError(f"a state does not fit its parameter with state_bits={bits}")
-            me = ve = 0
+            e, f = m, v
             if bits == 8:
                 e, f = state["exp_avg_exponent"], state["exp_avg_sq_exponent"]
-                blocks = -(-p.numel() // BLOCK)
-                if e.dtype != want or f.dtype != want or e.numel() != blocks or f.numel() != blocks or \
-                        not e.is_contiguous() or not f.is_contiguous():
+                blocks = -(-n // BLOCK)
+                if not (e.dtype is state_dtype and f.dtype is state_dtype and e.numel() == blocks and f.numel() == blocks and
+                        e.is_contiguous() and f.is_contiguous() and e.is_cuda and f.is_cuda):
                     raise ValueError("a state's exponents do not fit its parameter")
-                me, ve = e.data_ptr(), f.data_ptr()
-            t = None
             if not capturable:
-                t = state["step"] = int(state["step"]) + 1
-            calls.setdefault((p.device, t), []).append(
-                (p.data_ptr(), g.data_ptr(), m.data_ptr(), v.data_ptr(), me, ve, p.numel(),
-                 OUT_F32 if p.dtype == torch.float32 else OUT_BF16, first + i))
+                t = int(state["step"])
+                counted.append((state, t + 1))
+            rows = calls.get((p.device, t))
+            if rows is None:
+                rows = calls[p.device, t] = array.array("Q")
+            # the last word holds the struct's two 32-bit fields, dtype and id
+            rows.extend((p.data_ptr(), g.data_ptr(), m.data_ptr(), v.data_ptr(), e.data_ptr(), f.data_ptr(), n,
+                         (OUT_F32 if dtype is torch.float32 else OUT_BF16) | (first + i) << 32))
         if capturable:
             if len(calls) > 1:
                 raise ValueError("the parameters of a capturable group must be on one device")
-            (device, _), = calls
             count = group.get("step_count")
             if count is None:
                 if capturing:
                     raise RuntimeError("take one step before the capture: it creates the states")
                 count = group["step_count"] = torch.zeros((), dtype=torch.int64, device=device)
             count += 1
-        lr, (b1, b2) = group["lr"], group["betas"]
-        on_device = isinstance(lr, torch.Tensor)
+        for state, step in counted:
+            state["step"] = step
         for (device, t), rows in calls.items():
-            entries = np.array(rows, dtype=_ENTRY)
-            lib, lock = _shared_context(device)
-            with lock:
-                lib.adamw_step(entries.ctypes.data, len(rows), 0.0 if on_device else float(lr), b1, b2, group["eps"],
-                               group["weight_decay"], t or 1, bits, 1 if group["rounding"] == "sr" else 0, self.seed,
-                               lr_dev=lr if on_device else None, step_dev=group["step_count"] if capturable else None)
+            self._launch(group, device, t, rows)
+        # a plan for the next step where this one was regular
+        if len(calls) > 1 or keep or len(todo) != len(group["params"]) or not all(p.is_contiguous() for _, p, _ in todo):
+            return None
+        params, own = [p for _, p, _ in todo], [states[p] for _, p, _ in todo]
+        return _Plan(params, [p.dtype for p in params], [p.numel() for p in params],
+                     params + [s[k] for k in _KEYS[bits] for s in own], list(states.values()), own, rows, device)
+
+    @staticmethod
+    def _same_layout(p, g, keep):
+        """The gradient in the order of the parameter's memory; a copy is put into `keep`."""
+        if not _dense_layout(p):
+            raise ValueError("a parameter's elements must fill one stretch of memory")
+        if g.shape != p.shape:
+            raise ValueError("a gradient must have its parameter's shape")
+        if g.stride() != p.stride():
+            g = torch.empty_like(p, memory_format=torch.preserve_format).copy_(g)
+            keep.append(g)
+        return g

@@ -7,9 +7,15 @@ import subprocess
 from tests.conftest import ROOT
 
 
+def test_scratch_size_matches_the_header(metis_lib):
+    text = open(os.path.join(ROOT, "include", "metis.h")).read()
+    copies = int(text.split("#define METIS_INT8_SCRATCH_COPIES ")[1].split()[0])
+    assert metis_lib.INT8_SCRATCH == copies + 1
+
+
 def test_new_struct_layouts(metis_lib, tmp_path):
     mirror = {"metis_int8": metis_lib.Int8Struct, "metis_adamw_tensor": metis_lib.AdamWTensor,
-              "metis_adamw_params": metis_lib.AdamWParams}
+              "metis_adamw_params": metis_lib.AdamWParams, "metis_dense": metis_lib.Dense}
     lines = ["#include <stdio.h>", "#include <stddef.h>", '#include "%s"' % os.path.join(ROOT, "include", "metis.h"),
              "int main(void) {"]
     for name, cls in mirror.items():

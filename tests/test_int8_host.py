@@ -81,7 +81,8 @@ def test_adamw_without_gradients_does_nothing(metis_lib):
 
 
 def test_entry_layout_matches_the_struct(metis_lib):
+    """The optimizer fills the entries as eight 64-bit words each."""
     from spectral_quantized_gemm_b200 import optim
-    assert optim._ENTRY.itemsize == metis_lib.ctypes.sizeof(metis_lib.AdamWTensor)
-    for name, _ in metis_lib.AdamWTensor._fields_:
-        assert optim._ENTRY.fields[name][1] == getattr(metis_lib.AdamWTensor, name).offset
+    T = metis_lib.AdamWTensor
+    assert metis_lib.ctypes.sizeof(T) == 8 * optim.ENTRY_WORDS
+    assert [getattr(T, f).offset for f, _ in T._fields_] == [0, 8, 16, 24, 32, 40, 48, 56, 60]
