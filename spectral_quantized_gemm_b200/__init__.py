@@ -470,7 +470,6 @@ class Context:
 
     def int8_linear_fwd(self, X, W, Y, Xrow, Wcol, Xcol=None, Wrow=None):
         """Training forward pass Y = Q(X) Q(W): the operands are Int8Struct of the layer's buffers."""
-        self._same_device(X=X, W=W, Y=Y)
         x, w, (ptr, ldy, dtype) = self._dense_struct(X, "X"), self._dense_struct(W, "W"), _dense(Y, "Y")
         if Y.shape != (X.shape[0], W.shape[1]):
             raise ValueError("expected Y of X's rows and W's columns")
@@ -478,7 +477,6 @@ class Context:
 
     def int8_linear_bwd(self, D, Drow=None, Dcol=None, Xcol=None, Wrow=None, dX=None, dW=None):
         """Training backward pass: dX = Q(D) Q(W)^T and / or dW = Q(X)^T Q(D) (fp32)."""
-        self._same_device(D=D, dX=dX, dW=dW)
         xptr, ldx, xdtype = (None, 0, OUT_F32) if dX is None else _dense(dX, "dX")
         wptr, ldw, wdtype = (None, 0, OUT_F32) if dW is None else _dense(dW, "dW")
         if wdtype != OUT_F32:
@@ -488,8 +486,9 @@ class Context:
             raise ValueError("dX or dW of another shape than its operands'")
         self._call(_int8_bwd, self._dense_struct(D, "D"), Drow, Dcol, Xcol, Wrow, xptr, ldx, xdtype, wptr, ldw)
 
-    @staticmethod
-    def _dense_struct(M, name):
+    def _dense_struct(self, M, name):
+        if M.device != self.device:
+            raise ValueError(f"{name} is on {M.device}, the context on {self.device}")
         ptr, ld, dtype = _dense(M, name)
         return Dense(ptr, M.shape[0], M.shape[1], ld, dtype)
 

@@ -650,6 +650,10 @@ metis_status check_gemm_int8(metis_ctx* ctx, const metis_int8* A, const metis_in
   return METIS_OK;
 }
 
+metis_status clear_scratch(metis_ctx* ctx, const metis_int8* a, const metis_int8* b) {
+  return check_cuda(ctx, clear_int8_scratch(a, b, ctx->stream), "int8 scratch");
+}
+// The scratch of col is clear.
 metis_status quantize_int8(metis_ctx* ctx, const metis_dense* M, const metis_int8* row, const metis_int8* col) {
   return check_cuda(ctx, launch_quantize_i8(M->data, M->dtype == METIS_OUT_BF16, M->rows, M->cols, M->ld, row, col,
                                             ctx->status, ctx->sm_count, ctx->stream),
@@ -696,7 +700,8 @@ metis_status metis_quantize_int8(metis_ctx* ctx, const void* M, int64_t rows, in
     const metis_status s = check_quantize_int8(ctx, M, rows, cols, ld, dtype, rowwise, colwise);
     if (s != METIS_OK) return s;
     const metis_dense dense{M, rows, cols, ld, dtype};
-    return quantize_int8(ctx, &dense, rowwise, colwise);
+    const metis_status c = clear_scratch(ctx, colwise, nullptr);
+    return c == METIS_OK ? quantize_int8(ctx, &dense, rowwise, colwise) : c;
   });
 }
 
@@ -733,7 +738,9 @@ metis_status metis_int8_linear_fwd(metis_ctx* ctx, const metis_dense* X, const m
     if (s != METIS_OK || (s = check_quantize_int8(ctx, W->data, W->rows, W->cols, W->ld, W->dtype, Wrow, Wcol)) != METIS_OK ||
         (s = check_gemm_int8(ctx, Xrow, Wcol, Y, ldy, y_dtype)) != METIS_OK)
       return s;
-    if ((s = quantize_int8(ctx, X, Xrow, Xcol)) != METIS_OK || (s = quantize_int8(ctx, W, Wrow, Wcol)) != METIS_OK) return s;
+    if ((s = clear_scratch(ctx, Wcol, Xcol)) != METIS_OK || (s = quantize_int8(ctx, X, Xrow, Xcol)) != METIS_OK ||
+        (s = quantize_int8(ctx, W, Wrow, Wcol)) != METIS_OK)
+      return s;
     return launch_gemm_i8(ctx, Xrow, Wcol, Y, ldy, y_dtype, false);
   });
 }
@@ -750,7 +757,7 @@ metis_status metis_int8_linear_bwd(metis_ctx* ctx, const metis_dense* D, metis_i
     if (s != METIS_OK || (dX && (s = check_gemm_int8(ctx, Drow, Wrow, dX, lddx, dx_dtype)) != METIS_OK) ||
         (dW && (s = check_gemm_int8(ctx, Xcol, Dcol, dW, lddw, METIS_OUT_F32)) != METIS_OK))
       return s;
-    if ((s = quantize_int8(ctx, D, row, col)) != METIS_OK) return s;
+    if ((s = clear_scratch(ctx, col, nullptr)) != METIS_OK || (s = quantize_int8(ctx, D, row, col)) != METIS_OK) return s;
     if (dX && (s = launch_gemm_i8(ctx, Drow, Wrow, dX, lddx, dx_dtype, false)) != METIS_OK) return s;
     return dW ? launch_gemm_i8(ctx, Xcol, Dcol, dW, lddw, METIS_OUT_F32, false) : METIS_OK;
   });

@@ -23,6 +23,7 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <utility>
 
 #include "device_common.cuh"
 #include "internal.h"
@@ -504,7 +505,6 @@ cudaError_t run_quantize(const T* M, int64_t rows, int64_t cols, int64_t ld, con
   if (col) {
     tops = col->scratch;
     marks = col->scratch + kCopies * cols;
-    if ((e = cudaMemsetAsync(tops, 0, (size_t)cols * 4 * (kCopies + 1), st)) != cudaSuccess) return e;
   }
   if (row && cols > kMostHeld) {
     quantize_i8_long_rows_kernel<T><<<(unsigned)rows, 512, 0, st>>>(M, (int)cols, ld, row->codes, row->ld, row->scales, status);
@@ -536,6 +536,19 @@ cudaError_t run_quantize(const T* M, int64_t rows, int64_t cols, int64_t ld, con
 }
 
 }  // namespace
+
+cudaError_t clear_int8_scratch(const metis_int8* a, const metis_int8* b, cudaStream_t st) {
+  if (a && b && b->scratch + METIS_INT8_SCRATCH * b->outer == a->scratch) std::swap(a, b);
+  cudaError_t e = cudaSuccess;
+  size_t words = a ? (size_t)METIS_INT8_SCRATCH * a->outer : 0;
+  if (a && b && a->scratch + words == b->scratch) {   // side by side: one fill
+    words += (size_t)METIS_INT8_SCRATCH * b->outer;
+    b = nullptr;
+  }
+  if (a) e = cudaMemsetAsync(a->scratch, 0, words * 4, st);
+  if (b && e == cudaSuccess) e = cudaMemsetAsync(b->scratch, 0, (size_t)METIS_INT8_SCRATCH * b->outer * 4, st);
+  return e;
+}
 
 cudaError_t launch_quantize_i8(const void* M, bool bf16, int64_t rows, int64_t cols, int64_t ld, const metis_int8* row,
                                const metis_int8* col, uint32_t* status, int sm_count, cudaStream_t st) {

@@ -21,6 +21,7 @@ Any number of tokens and features is allowed (in_features, and out_features and 
 a backward pass, up to 131071, the bound of the exact sum).  There is no CPU path.
 """
 
+import functools
 import math
 
 import torch
@@ -44,23 +45,30 @@ def _operand(M):
     return M if M.stride(-1) == 1 or M.shape[-1] == 1 else M.contiguous()
 
 
-def _buffers(device, *sizes):
-    """One allocation for the operands of sizes (outer, inner, columns): their Int8Struct and the
-    tensor that holds them.  columns: quantized column-wise, so with the scratch for it."""
+@functools.lru_cache(maxsize=256)
+def _layout(sizes):
+    """Bytes of one allocation for the operands of sizes (outer, inner, columns), and where each has its codes,
+    scales and scratch in it.  columns: quantized column-wise, so with the scratch for that; the
+    scratches lie side by side, so that one fill clears them."""
     at, places = 0, []
     for outer, inner, columns in sizes:
         ld = -(-inner // 16) * 16
-        scales = at + outer * ld
-        places.append((at, scales, scales + 4 * outer, ld))
-        at = -(-(scales + 4 * outer * (1 + (INT8_SCRATCH if columns else 0))) // 256) * 256
-    buf = torch.empty(at, dtype=torch.uint8, device=device)
-    return buf, _views(buf, sizes, places)
+        places.append((at, at + outer * ld, ld))
+        at = -(-(at + outer * (ld + 4)) // 256) * 256
+    out = []
+    for (outer, inner, columns), (codes, scales, ld) in zip(sizes, places):
+        out.append((outer, inner, ld, codes, scales, at if columns else None))
+        at += 4 * outer * INT8_SCRATCH if columns else 0
+    return at, out
 
 
-def _views(buf, sizes, places):
+def _buffers(device, sizes):
+    """One allocation for the operands of sizes (outer, inner, columns), and their Int8Struct."""
+    total, places = _layout(sizes)
+    buf = torch.empty(total, dtype=torch.uint8, device=device)
     base = buf.data_ptr()
-    return [Int8Struct(base + codes, base + scales, outer, inner, ld, base + scratch if columns else None)
-            for (outer, inner, columns), (codes, scales, scratch, ld) in zip(sizes, places)]
+    return buf, [Int8Struct(base + codes, base + scales, outer, inner, ld, None if scratch is None else base + scratch)
+                 for outer, inner, ld, codes, scales, scratch in places]
 
 
 class _Int8LinearFn(torch.autograd.Function):
@@ -73,16 +81,18 @@ class _Int8LinearFn(torch.autograd.Function):
             return torch.empty(0, n, dtype=torch.bfloat16, device=x.device)
         x, w = _operand(x), _operand(weight)
         # what the backward pass reads is kept, the rest goes with this call
-        kept_sizes = ([(m, rows, True)] if need_dw else []) + ([(m, n, False)] if need_dx else [])
-        kept, saved = _buffers(x.device, *kept_sizes) if kept_sizes else (None, [])
-        work, (xr, wc) = _buffers(x.device, (rows, m, False), (n, m, True))
+        sizes = (((m, rows, False),) if need_dw else ()) + (((m, n, False),) if need_dx else ())
+        kept, saved = _buffers(x.device, sizes) if sizes else (None, [])
+        work, (xr, wc, *scratch) = _buffers(x.device, ((rows, m, False), (n, m, True)) + (((m, 1, True),) if need_dw else ()))
+        if need_dw:
+            saved[0].scratch = scratch[0].scratch
         y = _output(rows, n, torch.bfloat16, x.device)
         lib, lock = _shared_context(x.device)
         with lock:
             lib.int8_linear_fwd(x, w, y, xr, wc, Xcol=saved[0] if need_dw else None, Wrow=saved[-1] if need_dx else None)
         if kept is not None:
             ctx.save_for_backward(kept)
-            ctx.kept = [(s.outer, s.inner, s.ld, s.codes - kept.data_ptr(), s.scales - kept.data_ptr()) for s in saved]
+            ctx.kept = sizes
         return y
 
     @staticmethod
@@ -95,9 +105,10 @@ class _Int8LinearFn(torch.autograd.Function):
                     torch.zeros(m, n, dtype=ctx.w_dtype, device=dy.device) if need_dw else None)
         kept, = ctx.saved_tensors
         base = kept.data_ptr()
-        saved = [Int8Struct(base + codes, base + scales, outer, inner, ld, None) for outer, inner, ld, codes, scales in ctx.kept]
+        saved = [Int8Struct(base + codes, base + scales, outer, inner, ld, None)
+                 for outer, inner, ld, codes, scales, _ in _layout(ctx.kept)[1]]
         dy = _operand(dy)
-        work, new = _buffers(dy.device, *([(n, rows, True)] if need_dw else []), *([(rows, n, False)] if need_dx else []))
+        work, new = _buffers(dy.device, (((n, rows, True),) if need_dw else ()) + (((rows, n, False),) if need_dx else ()))
         dx = _output(rows, m, torch.bfloat16 if ctx.x_dtype == torch.bfloat16 else torch.float32, dy.device) if need_dx else None
         dw = _output(m, n, torch.float32, dy.device) if need_dw else None
         lib, lock = _shared_context(dy.device)
@@ -143,21 +154,21 @@ class Int8Linear(torch.nn.Module):
         return self
 
     def forward(self, x):
+        weight = self.weight
         if x.shape[-1] != self.in_features:
             raise ValueError(f"expected last dimension {self.in_features}, got {x.shape[-1]}")
-        if x.device != self.weight.device:
-            raise ValueError(f"x is on {x.device}, the weight on {self.weight.device}")
-        lead = x.shape[:-1]
-        flat = x.reshape(-1, self.in_features)
-        if torch.is_grad_enabled() and (x.requires_grad or self.weight.requires_grad):
+        if x.device != weight.device:
+            raise ValueError(f"x is on {x.device}, the weight on {weight.device}")
+        flat = x if x.dim() == 2 else x.reshape(-1, self.in_features)
+        if torch.is_grad_enabled() and (x.requires_grad or weight.requires_grad):
             if flat.shape[0] > MAX_INNER:
                 raise ValueError(f"at most {MAX_INNER} tokens in a pass with gradients, got {flat.shape[0]}")
-            y = _Int8LinearFn.apply(flat, self.weight)
+            y = _Int8LinearFn.apply(flat, weight)
         elif self._frozen is not None:
             y = self._serve(flat)
         else:
-            y = _Int8LinearFn.apply(flat.detach(), self.weight.detach())
-        return y.reshape(*lead, self.out_features)
+            y = _Int8LinearFn.apply(flat.detach(), weight.detach())
+        return y if x.dim() == 2 else y.reshape(*x.shape[:-1], self.out_features)
 
     def _serve(self, x):
         held, version = self._frozen
