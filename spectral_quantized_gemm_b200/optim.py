@@ -21,6 +21,7 @@ the states.  There is no CPU path.
 """
 
 import array
+import itertools
 import operator
 
 import torch
@@ -45,6 +46,11 @@ def _dense_layout(t):
     return True
 
 
+_address, _numel, _contiguous = torch.Tensor.data_ptr, torch.Tensor.numel, torch.Tensor.is_contiguous
+_grad, _dtype, _on_gpu = operator.attrgetter("grad"), operator.attrgetter("dtype"), operator.attrgetter("is_cuda")
+_step = operator.itemgetter("step")
+
+
 class _Plan:
     """The entries of a group's last step and the objects that they were made from.  The next step
     uses them again, with the addresses of its gradients, if every object is still the same and
@@ -56,26 +62,26 @@ class _Plan:
         self.where = self.addresses()
 
     def addresses(self):
-        return [t.data_ptr() for t in self.tensors]
+        return list(map(_address, self.tensors))
 
     def renew(self, params, all_states, keys, t):
         """Whether the plan holds; then its entries are those of the step t (None: not counted here)."""
         if len(params) != len(self.params) or not all(map(operator.is_, params, self.params)) or \
                 len(all_states) != len(self.all_states) or not all(map(operator.is_, all_states.values(), self.all_states)):
             return False
-        grads = [p.grad for p in params]
-        if any(g is None for g in grads) or [g.dtype for g in grads] != self.dtypes or \
-                [g.numel() for g in grads] != self.sizes or not all([g.is_contiguous() and g.is_cuda for g in grads]):
+        grads = list(map(_grad, params))
+        if any(map(operator.is_, grads, itertools.repeat(None))) or list(map(_dtype, grads)) != self.dtypes or \
+                list(map(_numel, grads)) != self.sizes or not all(map(_contiguous, grads)) or not all(map(_on_gpu, grads)):
             return False
-        if not all(map(operator.is_, self.tensors[len(params):], [s[k] for k in keys for s in self.states])) or \
-                self.addresses() != self.where:
+        now = itertools.chain.from_iterable(map(operator.itemgetter(k), self.states) for k in keys)
+        if not all(map(operator.is_, self.tensors[len(params):], now)) or self.addresses() != self.where:
             return False
         if t is not None:
-            if any([s["step"] != t for s in self.states]):
+            if list(map(_step, self.states)).count(t) != len(params):
                 return False
             for s in self.states:
                 s["step"] = t + 1
-        self.entries[1::ENTRY_WORDS] = array.array("Q", [g.data_ptr() for g in grads])
+        self.entries[1::ENTRY_WORDS] = array.array("Q", map(_address, grads))
         return True
 
 
