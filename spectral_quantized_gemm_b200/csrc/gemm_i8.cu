@@ -5,9 +5,10 @@
 // multiplied by sA[i] and by sB[j], then rounded to the output type.
 //
 // gemm_i8_kernel: a cluster of S CTAs computes one tile of 128 rows of B (channels, on the
-// lanes of tensor memory) by BN rows of A (tokens), each CTA a share of K; the int32 sums are
-// joined through distributed shared memory (the order of integer additions does not matter)
-// and every CTA writes its part of the tile.
+// lanes of tensor memory) by BN rows of A (tokens), each CTA a share of K.  Each CTA finishes
+// some of the tokens: the others send it their int32 sums of these by asynchronous stores to its
+// shared memory, whose bytes a barrier there counts, so nobody waits for a whole cluster (the
+// order of integer additions does not matter).
 //   warp 0      TMA producer, 128-byte swizzled tiles of 128 K elements; zeros past the edges
 //   warp 1      tensor-memory owner and MMA issuer (one thread)
 //   warps 2..5  epilogue
@@ -35,7 +36,7 @@
 namespace metis {
 namespace {
 
-constexpr int kThreads = 192;
+constexpr int kThreads = 192, kMaxSplits = 8;
 
 struct Params {
   const float* sa;
@@ -46,69 +47,66 @@ struct Params {
   int f32;
   int lane_tiles;        // 128-row blocks of B
   int k_tiles;           // 128-element blocks of K
-  int stages;            // of the ring
   int early;             // B may be read before the preceding kernel has ended
   uint32_t* status;
 };
 
-template <int BN>
+template <int BN, bool SPLIT>
 struct Cfg {
   static constexpr int A_BYTES = BN * 128;             // tokens
   static constexpr int B_BYTES = 128 * 128;            // channels
   static constexpr int STAGE_BYTES = A_BYTES + B_BYTES;
   static constexpr int TMEM_COLS = BN < 32 ? 32 : BN;
-  // Three CTAs fit an SM (BN 16 and 32), or two (64); a CTA that has its SM to itself takes a
-  // deeper ring.
-  static constexpr int STAGES = BN == 32 ? 3 : 4;
-  static constexpr int DEEP = STAGES;
-  static constexpr int PER_SM = BN == 64 ? 2 : 3;
+  // Two or three CTAs fit an SM.  (Rings of 8 or 12 stages for a CTA that has its SM to itself were
+  // no faster: 512 x 768 x 2304 7.1 us against 6.5.)
+  static constexpr int STAGES = SPLIT || BN == 32 ? 3 : 4;
+  static constexpr int PER_SM = BN == 16 || (BN == 32 && !SPLIT) ? 3 : 2;
   static constexpr int PITCH = 128 + 4;                // words of a staged row of sums
-  static constexpr int STAGED = BN * PITCH * 4;        // they take the ring's place
-  static constexpr int __host__ __device__ ring(int stages) {
-    return stages * STAGE_BYTES > STAGED ? stages * STAGE_BYTES : STAGED;
-  }
-  static constexpr size_t smem(int stages) { return (size_t)ring(stages) + (128 + BN) * 4 + 1024 + 256; }
-  static_assert(STAGED % 16 == 0 && (smem(STAGES) + 1024) * PER_SM <= 233472, "CTAs an SM");
-  static_assert(smem(DEEP) <= 232448, "shared memory budget");
+  // One CTA a tile: the sums take the ring's place.  Several: a place of their own, S times
+  // ceil(BN / S) rows, which may be written while this CTA still multiplies.
+  static constexpr int STAGED = (SPLIT ? BN + kMaxSplits - 1 : BN) * PITCH * 4;
+  static constexpr int RING = SPLIT || STAGES * STAGE_BYTES > STAGED ? STAGES * STAGE_BYTES : STAGED;
+  static constexpr size_t SMEM = (size_t)RING + (SPLIT ? STAGED : 0) + (128 + BN) * 4 + 1024 + 256;
+  static_assert(STAGED % 16 == 0 && (SMEM + 1024) * PER_SM <= 233472, "CTAs an SM");
 };
 
-__device__ __forceinline__ int4 load_cluster_int4(uint32_t addr) {
-  int4 v;
-  asm volatile("ld.shared::cluster.v4.s32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr) : "memory");
-  return v;
-}
-
-template <int BN, typename OUT>
+template <int BN, bool SPLIT, typename OUT>
 __global__ void __launch_bounds__(kThreads)
     gemm_i8_kernel(const __grid_constant__ CUtensorMap mapA, const __grid_constant__ CUtensorMap mapB, const Params p) {
-  using C = Cfg<BN>;
+  using C = Cfg<BN, SPLIT>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  float* sb = reinterpret_cast<float*>(smem + C::ring(p.stages));   // scales of the tile's channels and tokens
+  float* sb = reinterpret_cast<float*>(smem + C::RING + (SPLIT ? C::STAGED : 0));   // scales of the tile's channels and tokens
   float* sa = sb + 128;
   uint64_t* bars = reinterpret_cast<uint64_t*>(sb + 128 + BN);
   uint64_t* full = bars;
-  uint64_t* empty = bars + C::DEEP;
-  uint64_t* done = bars + 2 * C::DEEP;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(done + 1);
+  uint64_t* empty = bars + C::STAGES;
+  uint64_t* done = bars + 2 * C::STAGES;
+  uint64_t* received = done + 1;   // (SPLIT) the cluster's sums of this CTA's tokens are here
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(done + 2);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int splits = (int)tc::cluster_size();
-  const int split = (int)tc::cluster_rank();
+  const int splits = SPLIT ? (int)tc::cluster_size() : 1;
+  const int split = SPLIT ? (int)tc::cluster_rank() : 0;
   const int tile = blockIdx.x / splits;
   const int lb = tile % p.lane_tiles, cb = tile / p.lane_tiles;
   const int s0 = (int)((int64_t)p.k_tiles * split / splits), s1 = (int)((int64_t)p.k_tiles * (split + 1) / splits);
 
-  const int first = min(p.stages, s1 - s0);   // the first round of the ring
+  const int first = min(C::STAGES, s1 - s0);   // the first round of the ring
+  // tokens of the tile, and this CTA's: own0 .. own1 - 1
+  const int rows = (int)min((int64_t)BN, p.p - (int64_t)cb * BN), share = (BN + splits - 1) / splits;
+  const int own0 = min(rows, split * share), own1 = min(rows, own0 + share);
   if (threadIdx.x == 0) {
-    for (int s = 0; s < p.stages; ++s) {
+    for (int s = 0; s < C::STAGES; ++s) {
       tc::mbar_init(&full[s], 1);
       tc::mbar_init(&empty[s], 1);
     }
     tc::mbar_init(done, 1);
+    if (SPLIT) tc::mbar_init(received, 1);
     *abort_flag = 0;
     tc::fence_barrier_init();
+    if (SPLIT) tc::mbar_expect_tx(received, (uint32_t)(splits * (own1 - own0) * 128 * 4));
     // the first loads leave before the other threads are ready; B's also under the tail of the
     // preceding kernel
     for (int s = 0; s < first; ++s) {
@@ -123,6 +121,7 @@ __global__ void __launch_bounds__(kThreads)
   }
   tc::tc_fence_before();
   __syncthreads();
+  if (SPLIT) tc::cluster_arrive();   // this CTA's barrier is ready for the others' sums
   tc::tc_fence_after();
   const uint32_t tmem = *tmem_slot;
 
@@ -133,8 +132,8 @@ __global__ void __launch_bounds__(kThreads)
         for (int s = 0; s < first; ++s)
           tc::tma_load_2d(smem + s * C::STAGE_BYTES, &mapA, &full[s], (s0 + s) * 128, cb * BN);
       }
-      int stage = first == p.stages ? 0 : first, issued = first;
-      uint32_t phase = first == p.stages ? 1u : 0u;
+      int stage = first == C::STAGES ? 0 : first, issued = first;
+      uint32_t phase = first == C::STAGES ? 1u : 0u;
       for (int kk = s0 + first; kk < s1; ++kk) {
         if (!tc::mbar_wait(&empty[stage], phase ^ 1u, abort_flag)) {
           *abort_flag = 1;
@@ -145,16 +144,16 @@ __global__ void __launch_bounds__(kThreads)
         tc::mbar_expect_tx(&full[stage], C::STAGE_BYTES);
         tc::tma_load_2d(at + C::A_BYTES, &mapB, &full[stage], kk * 128, lb * 128);
         tc::tma_load_2d(at, &mapA, &full[stage], kk * 128, cb * BN);
-        if (++stage == p.stages) {
+        if (++stage == C::STAGES) {
           stage = 0;
           phase ^= 1u;
         }
         ++issued;
       }
       // after a timeout too, no load is in flight when the block goes on
-      for (int k = min(issued, p.stages); k > 0; --k) {
+      for (int k = min(issued, C::STAGES); k > 0; --k) {
         if (--stage < 0) {
-          stage = p.stages - 1;
+          stage = C::STAGES - 1;
           phase ^= 1u;
         }
         tc::mbar_wait(&full[stage], phase, nullptr);
@@ -178,7 +177,7 @@ __global__ void __launch_bounds__(kThreads)
 #pragma unroll
         for (int j = 0; j < 4; ++j) tc::mma_i8(tmem, lanes + 2 * j, cols + 2 * j, id, (kk != s0 || j) ? 1u : 0u);
         tc::tc_commit(&empty[stage]);
-        if (++stage == p.stages) {
+        if (++stage == C::STAGES) {
           stage = 0;
           phase ^= 1u;
         }
@@ -199,50 +198,69 @@ __global__ void __launch_bounds__(kThreads)
     if (p.early) tc::grid_dependency_wait();
     if (t < BN) sa[t] = (int64_t)cb * BN + t < p.p ? p.sa[(int64_t)cb * BN + t] : 0.0f;
   }
-  // All loads have landed and all MMAs are done once every thread is here: the ring's
-  // memory becomes the staging buffer.
+  // All loads have landed and all MMAs are done once every thread is here.
   tc::tc_fence_before();
   __syncthreads();
+  if (SPLIT) tc::cluster_wait();
   tc::tc_fence_after();
-  int* staged = reinterpret_cast<int*>(smem);
-  if (warp >= 2) {
+  int* staged = reinterpret_cast<int*>(smem + (SPLIT ? C::RING : 0));
+  if (warp >= 2 && !(SPLIT && *abort_flag)) {
     const int quarter = warp & 3;
     const int row = quarter * 32 + lane;
     constexpr int W = BN < 32 ? 16 : 32;
+    // (SPLIT) where the sums of the current token go: CTA 0's first
+    const uint32_t here = tc::smem_addr(staged + split * share * C::PITCH + row);
+    int owner = 0, left = share;
+    uint32_t to = SPLIT ? tc::cluster_addr_u32(here, 0) : 0u, bar = SPLIT ? tc::cluster_addr_u32(tc::smem_addr(received), 0) : 0u;
 #pragma unroll
     for (int c = 0; c < BN; c += W) {
       float f[W];
       const uint32_t addr = tmem + ((uint32_t)(quarter * 32) << 16) + (uint32_t)c;
       if constexpr (W == 16) tc::tmem_load_16cols(addr, f); else tc::tmem_load_32cols(addr, f);
       tc::tmem_load_wait();
+      if constexpr (SPLIT) {
 #pragma unroll
-      for (int i = 0; i < W; ++i) staged[(c + i) * C::PITCH + row] = __float_as_int(f[i]);
+        for (int i = 0; i < W; ++i) {
+          if (c + i < rows) tc::store_async(to, __float_as_uint(f[i]), bar);
+          to += C::PITCH * 4;
+          if (--left == 0) {                            // the next CTA's tokens
+            left = share;
+            ++owner;
+            to = tc::cluster_addr_u32(here, (uint32_t)min(owner, splits - 1));
+            bar = tc::cluster_addr_u32(tc::smem_addr(received), (uint32_t)min(owner, splits - 1));
+          }
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < W; ++i) staged[(c + i) * C::PITCH + row] = __float_as_int(f[i]);
+      }
     }
   }
   tc::tc_fence_before();
   __syncthreads();
-  if (splits > 1) tc::cluster_sync();
   if (warp == 1) {
     tc::tc_fence_after();
     tc::tmem_dealloc(tmem, C::TMEM_COLS);
   }
-  // This CTA's part of the tile: runs of 8 columns of C, a 16-byte store of bf16 or two of fp32.
-  // Kept small (one output type, not unrolled): a CTA runs it once, and unrolled four times its
+  // This CTA's tokens: runs of 8 columns of C, a 16-byte store of bf16 or two of fp32.  Kept
+  // small (one output type, not unrolled): a CTA runs it once, and unrolled four times its
   // instructions took 0.5 us longer to come in than they saved.
   if (warp >= 2) {
+    // After a timeout too, the wait lasts until nothing more can arrive here.
+    const bool here = !SPLIT || own1 == own0 || tc::mbar_wait_cluster(received, 0);
+    if (!here && lane == 0) raise_status(p.status, METIS_DEV_TIMEOUT);
+    const int end = here ? own1 * (128 / 8) : 0;
     constexpr int RUNS = 128 / 8;
-    const int rows = (int)min((int64_t)BN, p.p - (int64_t)cb * BN), cols = (int)min((int64_t)128, p.q - (int64_t)lb * 128);
+    const int cols = (int)min((int64_t)128, p.q - (int64_t)lb * 128);
     OUT* const c0 = static_cast<OUT*>(p.C) + (int64_t)cb * BN * p.ldc + (int64_t)lb * 128;
-    const uint32_t mine = tc::smem_addr(staged);
-    const int u1 = rows * RUNS * (split + 1) / splits;
-    for (int u = rows * RUNS * split / splits + (int)threadIdx.x - 64; u < u1; u += kThreads - 64) {
+    for (int u = own0 * RUNS + (int)threadIdx.x - 64; u < end; u += kThreads - 64) {
       const int i = u / RUNS, j = (u % RUNS) * 8;
       if (j >= cols) continue;
-      const uint32_t off = (uint32_t)(i * C::PITCH + j) * 4u;
-      int4 a = make_int4(0, 0, 0, 0), b = a;
-      for (int s = 0; s < splits; ++s) {
-        const uint32_t from = tc::cluster_addr_u32(mine + off, (uint32_t)s);
-        const int4 x = load_cluster_int4(from), y = load_cluster_int4(from + 16);
+      const int* from = staged + (i - own0) * C::PITCH + j;
+      int4 a = *reinterpret_cast<const int4*>(from), b = *reinterpret_cast<const int4*>(from + 4);
+      for (int s = 1; s < splits; ++s) {
+        from += share * C::PITCH;
+        const int4 x = *reinterpret_cast<const int4*>(from), y = *reinterpret_cast<const int4*>(from + 4);
         a.x += x.x; a.y += x.y; a.z += x.z; a.w += x.w;
         b.x += y.x; b.y += y.y; b.z += y.z; b.w += y.w;
       }
@@ -271,7 +289,6 @@ __global__ void __launch_bounds__(kThreads)
       }
     }
   }
-  if (splits > 1) tc::cluster_sync();   // no CTA leaves while its sums are still read
 }
 
 // ------------------------------------------------------------------ CTA-pair kernel
@@ -531,9 +548,9 @@ bool make_map_i8(CUtensorMap* map, const metis_int8* t, uint32_t box_rows) {
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int BN, typename OUT>
+template <int BN, bool SPLIT, typename OUT>
 metis_status launch_tile(metis_ctx* ctx, const metis_int8* A, const metis_int8* B, Params prm, int splits, bool chained) {
-  using C = Cfg<BN>;
+  using C = Cfg<BN, SPLIT>;
   CUtensorMap ma, mb;
   if (!make_map_i8(&ma, A, BN) || !make_map_i8(&mb, B, 128))
     return fail(ctx, METIS_ERR_CUDA, "cuTensorMapEncodeTiled failed for the int8 operands");
@@ -541,16 +558,14 @@ metis_status launch_tile(metis_ctx* ctx, const metis_int8* A, const metis_int8* 
   const int64_t ctas = lane_tiles * col_tiles * splits;
   if (ctas > INT32_MAX) return fail(ctx, METIS_ERR_SHAPE, "too many output tiles");
   prm.lane_tiles = (int)lane_tiles;
-  prm.stages = std::min(splits == 1 && ctas <= ctx->sm_count ? C::DEEP : C::STAGES, (prm.k_tiles + splits - 1) / splits);
-  const size_t smem = C::smem(prm.stages);
-  auto kern = gemm_i8_kernel<BN, OUT>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  auto kern = gemm_i8_kernel<BN, SPLIT, OUT>;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::SMEM);
   if (e != cudaSuccess) return check_cuda(ctx, e, "cudaFuncSetAttribute(int8 gemm)");
   prm.early = chained;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3((unsigned)ctas);
   cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = smem;
+  cfg.dynamicSmemBytes = C::SMEM;
   cfg.stream = ctx->stream;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -622,12 +637,13 @@ metis_status launch_gemm_i8(metis_ctx* ctx, const metis_int8* A, const metis_int
   // one CTA an SM and eight blocks of K each (40 x 4096 x 4096: 14.1, 10.3 in four, 12.6 in eight;
   // 512 x 2304 x 768: 9.6, 9.1 in two, 10.0 in three).
   const int64_t room = (bn == 16 ? ctx->sm_count * 27 / 10 : ctx->sm_count) / tiles;
-  const int splits = (int)std::max<int64_t>(1, std::min<int64_t>({8, room, prm.k_tiles / (bn == 16 ? 4 : 8)}));
+  const int splits = (int)std::max<int64_t>(1, std::min<int64_t>({kMaxSplits, room, prm.k_tiles / (bn == 16 ? 4 : 8)}));
   auto launch = [&](auto zero) {
     using OUT = decltype(zero);
-    if (bn == 16) return launch_tile<16, OUT>(ctx, A, B, prm, splits, chained);
-    if (bn == 32) return launch_tile<32, OUT>(ctx, A, B, prm, splits, chained);
-    return launch_tile<64, OUT>(ctx, A, B, prm, splits, chained);
+#define METIS_TILE(BN) \
+  (splits > 1 ? launch_tile<BN, true, OUT>(ctx, A, B, prm, splits, chained) : launch_tile<BN, false, OUT>(ctx, A, B, prm, 1, chained))
+    return bn == 16 ? METIS_TILE(16) : bn == 32 ? METIS_TILE(32) : METIS_TILE(64);
+#undef METIS_TILE
   };
   return prm.f32 ? launch(float{}) : launch(__nv_bfloat16{});
 }

@@ -266,6 +266,27 @@ __device__ __forceinline__ uint32_t cluster_addr_u32(uint32_t saddr, uint32_t ra
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar) {
   asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
+// Asynchronous store of a word to another CTA's shared memory of the cluster; its 4 bytes are counted
+// on the mbarrier `bar` of the same CTA (both shared::cluster addresses).
+__device__ __forceinline__ void store_async(uint32_t addr, uint32_t v, uint32_t bar) {
+  asm volatile("st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.u32 [%0], %1, [%2];" ::"r"(addr), "r"(v), "r"(bar)
+               : "memory");
+}
+// mbar_wait for a phase that other CTAs of the cluster complete: acquires at cluster scope.
+__device__ __forceinline__ bool mbar_wait_cluster(uint64_t* bar, uint32_t parity, long long limit = kWaitLimitCycles) {
+  const long long t0 = clock64();
+  while (true) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2, %3;\n\tselp.u32 %0, 1, 0, "
+        "p;\n\t}"
+        : "=r"(ok)
+        : "r"(smem_addr(bar)), "r"(parity), "r"(100000u)
+        : "memory");
+    if (ok) return true;
+    if (clock64() - t0 > limit) return false;
+  }
+}
 // Tile loads into this CTA's shared memory whose bytes are counted on the mbarrier at
 // shared::cluster address `bar`, which may belong to the other CTA of the pair; every
 // CTA loads only its own tiles from this GPU's memory.
