@@ -24,6 +24,7 @@
 
 #include "device_common.cuh"
 #include "internal.h"
+#include "tc.cuh"
 
 namespace metis {
 namespace {
@@ -521,6 +522,8 @@ __device__ __forceinline__ bool run_chunk(const Table<CAP>& tab, int which, int6
 template <typename T, int BITS, bool SR, int CAP>
 __global__ void __launch_bounds__(kThreads, BITS == 32 ? 5 : 3) adamw_kernel(const __grid_constant__ Table<CAP> tab) {
   __shared__ Step sh;
+  tc::grid_dependency_wait();
+  tc::grid_launch_dependents();
   if (threadIdx.x == 0) sh = make_step(tab.c);
   __syncthreads();
   const Step s = sh;
@@ -568,9 +571,7 @@ cudaError_t launch_cap(metis_ctx* ctx, const metis_adamw_tensor* const* ts, int 
   tab.count = count;
   tab.chunks = chunks;
   const int64_t grid = std::min<int64_t>(chunks, (int64_t)ctx->sm_count * (BITS == 32 ? 5 : 3));
-  adamw_kernel<T, BITS, SR, CAP><<<(unsigned)grid, kThreads, 0, ctx->stream>>>(tab);
-  count_launch();
-  return cudaGetLastError();
+  return launch_early(adamw_kernel<T, BITS, SR, CAP>, grid, kThreads, 0, ctx->stream, tab);
 }
 
 template <typename T, int BITS, bool SR>

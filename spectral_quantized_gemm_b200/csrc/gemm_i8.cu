@@ -107,8 +107,9 @@ __global__ void __launch_bounds__(kThreads)
     *abort_flag = 0;
     tc::fence_barrier_init();
     if (SPLIT) tc::mbar_expect_tx(received, (uint32_t)(splits * (own1 - own0) * 128 * 4));
-    // the first loads leave before the other threads are ready; B's also under the tail of the
+    // the first loads leave before the other threads are ready; in a chain B's under the tail of the
     // preceding kernel
+    if (!p.early) tc::grid_dependency_wait();
     for (int s = 0; s < first; ++s) {
       tc::mbar_expect_tx(&full[s], C::STAGE_BYTES);
       tc::tma_load_2d(smem + s * C::STAGE_BYTES + C::A_BYTES, &mapB, &full[s], (s0 + s) * 128, lb * 128);
@@ -194,8 +195,10 @@ __global__ void __launch_bounds__(kThreads)
     // the tile's scales, fetched while the sums are made
     const int t = (int)threadIdx.x - 64;
     const int64_t j = (int64_t)lb * 128 + t;
+    if (!p.early) tc::grid_dependency_wait();
     sb[t] = j < p.q ? p.sb[j] : 0.0f;
     if (p.early) tc::grid_dependency_wait();
+    tc::grid_launch_dependents();
     if (t < BN) sa[t] = (int64_t)cb * BN + t < p.p ? p.sa[(int64_t)cb * BN + t] : 0.0f;
   }
   // All loads have landed and all MMAs are done once every thread is here.
@@ -362,6 +365,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairCfg::THREADS, 1)
   tc::tc_fence_after();
   const uint32_t tmem = *tmem_slot;
 
+  tc::grid_dependency_wait();
+  tc::grid_launch_dependents();
   const int pair = blockIdx.x >> 1, npairs = gridDim.x >> 1;
   const int num_tiles = p.m_tiles * p.n_tiles;
 
@@ -562,23 +567,8 @@ metis_status launch_tile(metis_ctx* ctx, const metis_int8* A, const metis_int8* 
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::SMEM);
   if (e != cudaSuccess) return check_cuda(ctx, e, "cudaFuncSetAttribute(int8 gemm)");
   prm.early = chained;
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3((unsigned)ctas);
-  cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = C::SMEM;
-  cfg.stream = ctx->stream;
-  cudaLaunchAttribute attr[2];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = (unsigned)splits;
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = 1;
-  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[1].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = chained ? 2 : 1;
-  e = cudaLaunchKernelEx(&cfg, kern, ma, mb, prm);
+  e = launch_early_cluster(kern, ctas, kThreads, C::SMEM, splits, ctx->stream, ma, mb, prm);
   if (e != cudaSuccess) return check_cuda(ctx, e, "int8 gemm launch");
-  count_launch();
   return METIS_OK;
 }
 
@@ -605,9 +595,8 @@ metis_status launch_pair(metis_ctx* ctx, const metis_int8* A, const metis_int8* 
   const cudaError_t e = cudaFuncSetAttribute(gemm_i8_pair_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::SMEM);
   if (e != cudaSuccess) return check_cuda(ctx, e, "cudaFuncSetAttribute(int8 gemm pair)");
   const int grid = 2 * (int)std::min<int64_t>(m_tiles * n_tiles, ctx->sm_count / 2);
-  gemm_i8_pair_kernel<<<grid, C::THREADS, C::SMEM, ctx->stream>>>(ma, mb, mc, pp);
-  count_launch();
-  return check_cuda(ctx, cudaGetLastError(), "int8 gemm pair launch");
+  return check_cuda(ctx, launch_early(gemm_i8_pair_kernel, grid, C::THREADS, C::SMEM, ctx->stream, ma, mb, mc, pp),
+                    "int8 gemm pair launch");
 }
 
 }  // namespace

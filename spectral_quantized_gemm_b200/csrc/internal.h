@@ -7,6 +7,7 @@
 #include <atomic>
 #include <cstdint>
 #include <string>
+#include <utility>
 #include <vector>
 
 #include "../../include/metis.h"
@@ -54,6 +55,35 @@ struct Workspace {
 metis_status ensure_workspace(metis_ctx* ctx, size_t bytes);
 metis_status fail(metis_ctx* ctx, metis_status s, const std::string& msg);
 metis_status check_cuda(metis_ctx* ctx, cudaError_t e, const char* what);
+
+// Launches a kernel that may start under the tail of the one before it on the stream (programmatic
+// dependent launch): it calls griddepcontrol.wait before it touches what that one writes or reads.
+// cluster: CTAs of a cluster.
+template <typename... P, typename... A>
+cudaError_t launch_early_cluster(void (*kern)(P...), int64_t blocks, int threads, size_t smem, int cluster, cudaStream_t st,
+                                 A&&... args) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3((unsigned)blocks);
+  cfg.blockDim = dim3((unsigned)threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = (unsigned)cluster;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, P(args)...);
+  if (e == cudaSuccess) count_launch();
+  return e;
+}
+template <typename... P, typename... A>
+cudaError_t launch_early(void (*kern)(P...), int64_t blocks, int threads, size_t smem, cudaStream_t st, A&&... args) {
+  return launch_early_cluster(kern, blocks, threads, smem, 1, st, std::forward<A>(args)...);
+}
 
 // cuTensorMapEncodeTiled, fetched from the driver through the runtime.
 using EncodeTiledFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
@@ -176,8 +206,8 @@ cudaError_t clear_int8_scratch(const metis_int8* a, const metis_int8* b, cudaStr
 cudaError_t launch_quantize_i8(const void* M, bool bf16, int64_t rows, int64_t cols, int64_t ld, const metis_int8* row,
                                const metis_int8* col, uint32_t* status, int sm_count, cudaStream_t st);
 // ---- gemm_i8.cu ----
-// chained: the launch before it on the stream is the quantizer that wrote A, itself an ordinary
-// launch, so that B is complete when this kernel starts early.
+// chained: the launch before it on the stream is the quantizer that wrote A, which lets this kernel start
+// only when all before the quantizer is complete, B with it.
 metis_status launch_gemm_i8(metis_ctx* ctx, const metis_int8* A, const metis_int8* B, void* C, int64_t ldc,
                             int32_t c_dtype, bool chained);
 // ---- adamw.cu ----

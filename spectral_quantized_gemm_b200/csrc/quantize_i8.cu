@@ -237,7 +237,8 @@ __global__ void __launch_bounds__(kRowBlock<GROUP, TOPS>, kRowBlocks<T, GROUP, H
   constexpr int BLOCK = kRowBlock<GROUP, TOPS>, GROUPS = BLOCK / GROUP, VECS = (int)sizeof(T) / 2;
   __shared__ uint32_t part[2][2][BLOCK / 32];
   extern __shared__ __align__(16) uint4 col[];   // [HELD][VECS][BLOCK]
-  tc::grid_launch_dependents();   // what follows may start loading
+  tc::grid_dependency_wait();     // only now, so that whatever follows early finds all before this complete
+  tc::grid_launch_dependents();
   const int t = threadIdx.x % GROUP, group = threadIdx.x / GROUP;
   const int64_t step = (int64_t)gridDim.x * GROUPS;
   int64_t r = (int64_t)blockIdx.x * GROUPS + group;
@@ -336,6 +337,7 @@ __global__ void __launch_bounds__(512) quantize_i8_long_rows_kernel(const T* __r
                                                                     int8_t* __restrict__ codes, int64_t ldq,
                                                                     float* __restrict__ scales, uint32_t* status) {
   __shared__ uint32_t part[2][16];
+  tc::grid_dependency_wait();
   tc::grid_launch_dependents();
   const int64_t r = blockIdx.x;
   const T* row = M + r * ld;
@@ -408,6 +410,7 @@ __global__ void __launch_bounds__(kThreads, 4) quantize_i8_cols_kernel(const T* 
     }
   }
   tc::grid_dependency_wait();   // for the maxima
+  tc::grid_launch_dependents();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int word = warp * 4 + (lane & 3);
   const int64_t c = c0 + word * PER_WORD;
@@ -458,6 +461,7 @@ __global__ void __launch_bounds__(kThreads, 4) quantize_i8_cols_kernel(const T* 
 }
 
 // ---------------------------------------------------------------- launches
+// All kernels here are launched so that they may start under the tail of the one before.
 template <typename T, int GROUP, int HELD, bool TOPS>
 cudaError_t launch_rows(const T* M, int64_t rows, int64_t cols, int64_t ld, const metis_int8* q, uint32_t* tops,
                         int64_t pitch, uint32_t* marks, uint32_t* status, int sm_count, cudaStream_t st) {
@@ -469,10 +473,8 @@ cudaError_t launch_rows(const T* M, int64_t rows, int64_t cols, int64_t ld, cons
     const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM);
     if (e != cudaSuccess) return e;
   }
-  kern<<<(unsigned)blocks, BLOCK, SMEM, st>>>(M, rows, (int)cols, ld, q ? q->codes : nullptr, q ? q->ld : 0,
-                                              q ? q->scales : nullptr, tops, pitch, marks, status);
-  count_launch();
-  return cudaGetLastError();
+  return launch_early(kern, blocks, BLOCK, SMEM, st, M, rows, (int)cols, ld, q ? q->codes : nullptr, q ? q->ld : 0,
+                      q ? q->scales : nullptr, tops, pitch, marks, status);
 }
 
 // A thread holds 64 bytes of a row, or 128 for the longest fp32 rows: the smallest group that
@@ -507,9 +509,8 @@ cudaError_t run_quantize(const T* M, int64_t rows, int64_t cols, int64_t ld, con
     marks = col->scratch + kCopies * cols;
   }
   if (row && cols > kMostHeld) {
-    quantize_i8_long_rows_kernel<T><<<(unsigned)rows, 512, 0, st>>>(M, (int)cols, ld, row->codes, row->ld, row->scales, status);
-    count_launch();
-    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    e = launch_early(quantize_i8_long_rows_kernel<T>, rows, 512, 0, st, M, (int)cols, ld, row->codes, row->ld, row->scales, status);
+    if (e != cudaSuccess) return e;
   }
   if (!col) return cols > kMostHeld ? e : run_rows<T, false>(M, rows, cols, ld, row, nullptr, 0, nullptr, status, sm_count, st);
   if (row && cols <= kMostHeld) {
@@ -520,19 +521,8 @@ cudaError_t run_quantize(const T* M, int64_t rows, int64_t cols, int64_t ld, con
   }
   if (e != cudaSuccess) return e;
   constexpr int COLS = kRowBytes / (int)sizeof(T);
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3((unsigned)((cols + COLS - 1) / COLS * ((rows + kTileRows - 1) / kTileRows)));
-  cfg.blockDim = dim3(kThreads);
-  cfg.stream = st;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  e = cudaLaunchKernelEx(&cfg, quantize_i8_cols_kernel<T>, M, rows, cols, ld, col->codes, col->ld, col->scales,
-                         (const uint32_t*)tops, (const uint32_t*)marks);
-  if (e == cudaSuccess) count_launch();
-  return e;
+  return launch_early(quantize_i8_cols_kernel<T>, (cols + COLS - 1) / COLS * ((rows + kTileRows - 1) / kTileRows), kThreads, 0, st,
+                      M, rows, cols, ld, col->codes, col->ld, col->scales, (const uint32_t*)tops, (const uint32_t*)marks);
 }
 
 }  // namespace
