@@ -105,10 +105,11 @@ __device__ Step make_step(const Coef& c) {
 }
 
 // Root and reciprocal within 2^-23 and 2^-22.  Flushing a subnormal v (root below 2^-63) to 0 does
-// not show beside an eps of 1e-11; with a smaller one the slower forms keep it.
+// not show beside an eps of 1e-11; with a smaller one (TINY) the slower forms keep it.
+template <bool TINY>
 __device__ __forceinline__ float stepped(float p, float m, float v, const Step& s) {
   float root, q;
-  if (!s.tiny) {
+  if constexpr (!TINY) {
     asm("sqrt.approx.ftz.f32 %0, %1;" : "=f"(root) : "f"(v));
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(q) : "f"(fmaf(root, s.rbc2, s.eps)));
     q *= m;
@@ -297,8 +298,10 @@ struct Block4 {
   int tm, tv;      // exponent bytes - 127
 };
 
-__device__ __forceinline__ uint32_t pack4(const uint32_t (&c)[4]) {
-  return __byte_perm(__byte_perm(c[0], c[1], 0x0040), __byte_perm(c[2], c[3], 0x0040), 0x5410);
+// The low eight bits above bit 20 of each, packed.
+__device__ __forceinline__ uint32_t codes4(const uint32_t (&r)[4]) {
+  const uint32_t a = __byte_perm(r[0], r[1], 0x7632) >> 4, b = __byte_perm(r[2], r[3], 0x7632) >> 4;
+  return __byte_perm(a, b, 0x6420);
 }
 
 // Steps the block's parameters in place and gives its new codes and exponents.  Returns whether a
@@ -308,24 +311,25 @@ __device__ __forceinline__ bool step_block(Block4& x, const Step& s, double b1, 
   // The fp32 route holds for exponents within these, where no scale leaves fp32's range and a
   // block's sums stay normal.
   const bool usual = x.tm <= 14 && x.tv <= 30;
+  // the coefficients of the codes as they are: exact, the decoding factors are powers of two
   const float dm = power2f(min(x.tm, 14) + 112), dv = power2f(min(x.tv, 30) + 96);
+  const float b1m = s.b1 * dm, b1m_low = s.b1_low * dm, b2v = s.b2 * dv;
   float ym[4], yv[4];
-  float hm = 0.0f, hv = 0.0f, z = 0.0f;
+  float hm = 0.0f;
+  uint32_t hv = 0;
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
-    const uint32_t mag = (j < 3 ? x.cm << (20 - 8 * j) : x.cm >> 4) & 0x07F00000u, neg = (x.cm << (24 - 8 * j)) & 0x80000000u;
-    const uint32_t vbits = (j < 3 ? x.cv << (20 - 8 * j) : x.cv >> 4) & 0x0FF00000u;
-    const float g = x.g[j], om = __uint_as_float(mag | neg) * dm;
-    z = fmaf(g, 0.0f, z);                            // NaN if any is not finite
-    // b1 m: exact for the upper 20 bits of b1 (m has four); (1 - b1) g: product and remainder
-    const float old = s.b1 * om, add = s.a1 * g;
-    float rest = fmaf(s.a1, g, -add);
-    rest = fmaf(s.a1_low, g, rest);
-    rest = fmaf(s.b1_low, om, rest);
-    const float sum = __fadd_rn(old, add), part = __fsub_rn(sum, old);
-    rest += __fadd_rn(__fsub_rn(old, __fsub_rn(sum, part)), __fsub_rn(add, part));   // what the sum dropped
-    ym[j] = sum + rest;
-    yv[j] = fmaf(s.b2, __uint_as_float(vbits) * dv, s.a2 * (g * g));   // four roundings: two units
+    // code j in the top byte, then its sign and magnitude in place
+    const int top = (int)__byte_perm(x.cm, 0u, (j << 12) | 0x0444u);
+    const float om = __uint_as_float((uint32_t)(top >> 4) & 0x87F00000u);
+    const float ov = __uint_as_float(__byte_perm(x.cv, 0u, (j << 12) | 0x0444u) >> 4);
+    const float g = x.g[j];
+    // b1 m + (1 - b1) g: the first product exact within the sum (m has four bits, the coefficient
+    // twenty), the second with its remainder; two roundings of the sum, so two units
+    const float add = s.a1 * g;
+    const float rest = fmaf(b1m_low, om, fmaf(s.a1_low, g, fmaf(s.a1, g, -add)));
+    ym[j] = fmaf(b1m, om, add) + rest;
+    yv[j] = fmaf(b2v, ov, s.a2 * (g * g));   // five roundings: three units
   }
   if (!usual) {
 #pragma unroll
@@ -338,19 +342,27 @@ __device__ __forceinline__ bool step_block(Block4& x, const Step& s, double b1, 
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
     hm = fmaxf(hm, fabsf(ym[j]));
-    hv = fmaxf(hv, yv[j]);
-    x.p[j] = stepped(x.p[j], ym[j], yv[j], s);
+    hv = max(hv, __float_as_uint(yv[j]));   // a NaN's bits lie above all others
   }
-  // the block's exponents (bits of positive floats order like them), open next to a power of two
-  const uint32_t top_m = __reduce_max_sync(0xffffffffu, __float_as_uint(hm)), top_v = __reduce_max_sync(0xffffffffu, __float_as_uint(hv));
+  if (!s.tiny) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) x.p[j] = stepped<false>(x.p[j], ym[j], yv[j], s);
+  } else {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) x.p[j] = stepped<true>(x.p[j], ym[j], yv[j], s);
+  }
+  // the block's exponents (bits of positive floats order like them), open next to a power of two and
+  // beyond the range, where gradients that are not finite end up too
+  const uint32_t top_m = __reduce_max_sync(0xffffffffu, __float_as_uint(hm)), top_v = __reduce_max_sync(0xffffffffu, hv);
   int tm = (int)(top_m >> 23) - 127, tv = (int)(top_v >> 23) - 127;
   const uint32_t edge = min((top_m + kNear) & 0x7FFFFFu, (top_v + kNear) & 0x7FFFFFu);
-  const bool odd = z != z;
-  const bool open = !usual || __any_sync(0xffffffffu, odd) || tm > 14 || tm < -60 || tv > 30 || tv < -60 || edge <= 2 * kNear;
+  const bool open = !usual || tm > 14 || tm < -60 || tv > 30 || tv < -60 || edge <= 2 * kNear;
+  bool odd = false;
   uint32_t om, ov, redo = 0;
   if (open) {
     om = ov = 0;
     const bool some = (x.cm | x.cv) != 0u || x.g[0] != 0.0f || x.g[1] != 0.0f || x.g[2] != 0.0f || x.g[3] != 0.0f;
+    odd = !isfinite(x.g[0]) || !isfinite(x.g[1]) || !isfinite(x.g[2]) || !isfinite(x.g[3]);
     if (!__any_sync(0xffffffffu, some)) {   // nothing there, and nothing new
       tm = tv = -111;
     } else {
@@ -366,30 +378,30 @@ __device__ __forceinline__ bool step_block(Block4& x, const Step& s, double b1, 
     }
   } else {
     const float sm = power2f(-112 - tm), sv = power2f(-96 - tv);
-    uint32_t rm[4], rv[4], cm[4], cv[4], near = 0xFFFFFu;
+    uint32_t rm[4], rv[4], near = 0xFFFFFFFFu;
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       rm[j] = rounded<SR>(__float_as_uint(fabsf(ym[j]) * sm), (w.w[j] << 4) & 0xFFFF0u);
       rv[j] = rounded<SR>(__float_as_uint(yv[j] * sv), (w.w[j] >> 12) & 0xFFFF0u);
-      near = min(near, min((rm[j] + kNear) & 0xFFFFFu, (rv[j] + kNear) & 0xFFFFFu));
-      cm[j] = rm[j] >> 20;
-      cv[j] = min(rv[j] >> 20, 255u);
+      near = min(near, min(rm[j] * 4096u + kNear * 4096u, rv[j] * 4096u + kNear * 4096u));   // the low 20 bits
     }
-    om = pack4(cm);
+    om = codes4(rm);
     om -= (om & 0x80808080u) >> 7;                   // 128, past the top code, becomes 127
-    const uint32_t b[4] = {__float_as_uint(ym[0]) >> 24, __float_as_uint(ym[1]) >> 24, __float_as_uint(ym[2]) >> 24, __float_as_uint(ym[3]) >> 24};
-    om |= (om + 0x7F7F7F7Fu) & pack4(b) & 0x80808080u;   // signs of codes that are not zero
-    ov = pack4(cv);
-    if (near <= 2 * kNear) {
+    const uint32_t signs = __byte_perm(__byte_perm(__float_as_uint(ym[0]), __float_as_uint(ym[1]), 0x0073),
+                                       __byte_perm(__float_as_uint(ym[2]), __float_as_uint(ym[3]), 0x0073), 0x5410);
+    om |= (om + 0x7F7F7F7Fu) & signs & 0x80808080u;  // of codes that are not zero
+    ov = codes4(rv);
+    if (near <= 2 * kNear * 4096u) {
 #pragma unroll
       for (int j = 0; j < 4; ++j)
-        if (min((rm[j] + kNear) & 0xFFFFFu, (rv[j] + kNear) & 0xFFFFFu) <= 2 * kNear) redo |= 1u << j;
+        if (min(rm[j] * 4096u + kNear * 4096u, rv[j] * 4096u + kNear * 4096u) <= 2 * kNear * 4096u) redo |= 1u << j;
     }
-    if ((ov - 0x01010101u) & ~ov & 0x80808080u) {    // a zero code of v: 1 where v is positive
+    if ((ov - 0x01010101u) & ~ov & 0x80808080u) {    // a zero code of v: 1 where v is positive, 255 where it was 256
 #pragma unroll
       for (int j = 0; j < 4; ++j)
         if (!((ov >> (8 * j)) & 255u)) {
-          if (yv[j] > 0.0f) ov |= 1u << (8 * j);
+          if (rv[j] >> 28) ov |= 255u << (8 * j);
+          else if (yv[j] > 0.0f) ov |= 1u << (8 * j);
           else if (x.g[j] != 0.0f || (x.cv >> (8 * j)) & 255u) redo |= 1u << j;   // fp64 may see more
         }
     }
@@ -450,7 +462,7 @@ __device__ __forceinline__ bool run_chunk(const Table<CAP>& tab, int which, int6
         z = fmaf(g, 0.0f, z);
         xm[j] = fmaf(s.b1, old, fmaf(s.b1_low, old, s.a1 * g));
         xv[j] = fmaf(s.b2, fv.get(j), s.a2 * (g * g));
-        xp[j] = stepped(fp.get(j), xm[j], xv[j], s);
+        xp[j] = s.tiny ? stepped<true>(fp.get(j), xm[j], xv[j], s) : stepped<false>(fp.get(j), xm[j], xv[j], s);
       }
       bad |= z != z;
       store4(m, i, FAST ? i + 4 : a.n, FAST || a.vec_s, xm);
