@@ -403,11 +403,12 @@ __global__ void __launch_bounds__(kThreads, 4) quantize_i8_cols_kernel(const T* 
     for (int r = threadIdx.x >> 3; r < n; r += kThreads / 8, src += (kThreads / 8) * ld)
       copy_async16(data + (r / kPiece) * kPieceBytes + (r % kPiece) * kRowBytes + chunk * 16, src);
   } else {
-    for (int e = threadIdx.x; e < n * COLS; e += kThreads) {
-      const int r = e / COLS, j = e % COLS;
-      if (c0 + j < cols)
-        *(reinterpret_cast<T*>(data + (r / kPiece) * kPieceBytes + (r % kPiece) * kRowBytes) + j) = M[(r0 + r) * ld + c0 + j];
-    }
+    const int j = threadIdx.x % COLS;
+    const T* src = M + (r0 + threadIdx.x / COLS) * ld + c0 + j;
+    if (c0 + j < cols)
+#pragma unroll 8
+      for (int r = threadIdx.x / COLS; r < n; r += kThreads / COLS, src += (kThreads / COLS) * ld)
+        *(reinterpret_cast<T*>(data + (r / kPiece) * kPieceBytes + (r % kPiece) * kRowBytes) + j) = *src;
   }
   tc::grid_dependency_wait();   // for the maxima
   tc::grid_launch_dependents();

@@ -17,6 +17,10 @@ keeps the codes of X and W, not X itself.
 Serving: ``freeze()`` lays the 8-bit weight out once; calls without gradients then read it
 instead of quantizing the weight each time, until ``unfreeze()``.
 
+To capture a training pass into a CUDA graph, run it once on the capturing stream first and let no
+graph of an earlier pass over the same leaves live on (torch's own rule: their gradients would be
+gathered on that pass's stream).
+
 Any number of tokens and features is allowed (in_features, and out_features and tokens of
 a backward pass, up to 131071, the bound of the exact sum).  There is no CPU path.
 """
@@ -42,7 +46,10 @@ def _operand(M):
     """M as the quantizer reads it: fp32 or bf16, unit stride along a row."""
     if M.dtype not in (torch.float32, torch.bfloat16):
         M = M.float()
-    return M if M.stride(-1) == 1 or M.shape[-1] == 1 else M.contiguous()
+    rows, cols = M.shape
+    if (M.stride(1) == 1 or cols == 1) and (M.stride(0) >= cols or rows == 1):
+        return M
+    return M.contiguous()     # transposed, or rows that are one and the same (an expanded gradient)
 
 
 @functools.lru_cache(maxsize=256)
@@ -146,8 +153,17 @@ class Int8Linear(torch.nn.Module):
         with lock:
             held = lib.new_int8(self.out_features, self.in_features)
             lib.quantize_int8(_operand(self.weight.detach()), colwise=held)
-        self._frozen = (held, self.weight._version)
+        self._frozen = (held, self._weight_mark())
         return self
+
+    def _weight_mark(self):
+        """Differs once the weight was written, replaced, cast or moved through torch (a replayed graph
+        that writes it is not seen)."""
+        w = self.weight
+        return w._version, w.data_ptr(), w.dtype, w.device
+
+    def __getstate__(self):
+        return dict(self.__dict__, _frozen=None)     # a copy lays its weight out itself
 
     def unfreeze(self):
         self._frozen = None
@@ -171,8 +187,8 @@ class Int8Linear(torch.nn.Module):
         return y if x.dim() == 2 else y.reshape(*x.shape[:-1], self.out_features)
 
     def _serve(self, x):
-        held, version = self._frozen
-        if version != self.weight._version or held.codes.device != self.weight.device:
+        held, mark = self._frozen
+        if mark != self._weight_mark():
             raise RuntimeError("the weight changed since freeze(); call freeze() or unfreeze()")
         rows = x.shape[0]
         if rows == 0:

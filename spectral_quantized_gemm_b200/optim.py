@@ -49,6 +49,9 @@ def _dense_layout(t):
 _address, _numel, _contiguous = torch.Tensor.data_ptr, torch.Tensor.numel, torch.Tensor.is_contiguous
 _grad, _dtype, _on_gpu = operator.attrgetter("grad"), operator.attrgetter("dtype"), operator.attrgetter("is_cuda")
 _step = operator.itemgetter("step")
+# The parameters are written behind torch's back; whoever compares versions (autograd's check of saved
+# tensors, a frozen layer) learns of it here.
+_increment_version = torch.autograd.graph.increment_version
 
 
 class _Plan:
@@ -165,6 +168,8 @@ class AdamW(torch.optim.Optimizer):
             with torch.enable_grad():
                 loss = closure()
         plans = self.__dict__.setdefault("_plans", {})
+        if len(plans) > len(self.param_groups):                 # groups have gone or changed their options
+            plans.clear()
         first = 0
         for number, group in enumerate(self.param_groups):
             plan = plans.get((number, first, group["state_bits"], group["capturable"]))
@@ -174,9 +179,7 @@ class AdamW(torch.optim.Optimizer):
         return loss
 
     def __getstate__(self):
-        state = super().__getstate__()
-        state.pop("_plans", None)
-        return state
+        return dict(super().__getstate__(), seed=self.seed)     # the plans stay behind
 
     def _step_again(self, group, plan):
         """The step from a plan that still holds; False if it does not."""
@@ -188,6 +191,7 @@ class AdamW(torch.optim.Optimizer):
         if t is None:
             group["step_count"] += 1
         self._launch(group, plan.device, t, plan.entries)
+        _increment_version(plan.params)
         return True
 
     def _launch(self, group, device, t, rows):
@@ -263,6 +267,7 @@ class AdamW(torch.optim.Optimizer):
             state["step"] = step
         for (device, t), rows in calls.items():
             self._launch(group, device, t, rows)
+        _increment_version([p for _, p, _ in todo])
         # a plan for the next step where this one was regular
         if len(calls) > 1 or keep or len(todo) != len(group["params"]) or not all(p.is_contiguous() for _, p, _ in todo):
             return None

@@ -323,6 +323,84 @@ def test_captured_steps_count_and_schedule_on_the_device(metis_lib, bits):
         assert torch.equal(opt.state[p]["exp_avg_sq"], want.state[q]["exp_avg_sq"])
 
 
+def test_what_moves_between_steps_is_followed(metis_lib):
+    """Steps after the first use what the last one gathered, unless something lies elsewhere now: new
+    gradients, a parameter or state with new memory, replaced states, a gradient in another order, a
+    missing one, changed options."""
+    import copy
+    from spectral_quantized_gemm_b200.optim import AdamW
+    params = _params([(500,), (30, 40), (130,)], torch.float32, 11)
+    hyper = dict(HYPER)
+    opt = AdamW(params, state_bits=8, rounding="rn", **hyper)
+    refs = [Reference(p, i, 8, "rn", 0) for i, p in enumerate(params)]
+
+    def step(seed, hyper=hyper):
+        _run(opt, params, refs, 1, hyper, first=seed)
+
+    for s in range(3):
+        step(s)
+    with torch.no_grad():
+        params[0].data = params[0].data.clone()
+    step(3)
+    opt.state[params[1]]["exp_avg"] = opt.state[params[1]]["exp_avg"].clone()
+    step(4)
+    opt.state[params[2]]["exp_avg_exponent"].data = opt.state[params[2]]["exp_avg_exponent"].clone()
+    step(5)
+    opt.state[params[0]] = copy.deepcopy(opt.state[params[0]])
+    step(6)
+    opt.load_state_dict(opt.state_dict())
+    step(7)
+    hyper = dict(hyper, lr=1e-2, betas=(0.8, 0.9), weight_decay=0.0)
+    opt.param_groups[0].update(hyper)
+    step(8, hyper)
+    # a gradient in another order, then the usual one
+    _run(opt, params, refs, 1, hyper, lambda p, s: _gradient(p, s).t().contiguous().t() if p.dim() == 2 else _gradient(p, s), first=9)
+    step(10, hyper)
+    # a parameter without a gradient falls a step behind and keeps its own count
+    before = [_np(_flat(p)) for p in params]
+    for i, p in enumerate(params):
+        p.grad = None if i == 1 else _gradient(p, 900 + i)
+    opt.step()
+    for i in (0, 2):
+        refs[i].step(before[i], _np(params[i].grad), params[i], opt.state[params[i]], hyper, False)
+    assert np.array_equal(_np(_flat(params[1])), before[1])
+    step(12, hyper)
+    step(13, hyper)
+    assert [opt.state[p]["step"] for p in params] == [14, 13, 14]
+
+
+def test_copies_of_the_optimizer_keep_their_stream(metis_lib):
+    import copy
+    import pickle
+    from spectral_quantized_gemm_b200.optim import AdamW
+    results = []
+    for how in (lambda x: x, copy.deepcopy, lambda x: pickle.loads(pickle.dumps(x))):
+        params = _params([(300,)], torch.float32, 12)
+        opt = AdamW(params, state_bits=8, seed=99, **HYPER)
+        for s in range(4):
+            if s == 2:
+                opt = how(opt)
+                params = opt.param_groups[0]["params"]
+            params[0].grad = _gradient(params[0], s)
+            opt.step()
+        results.append((params[0].detach().clone(), opt.state[params[0]]["exp_avg_sq"].clone()))
+    for p, v in results[1:]:
+        assert torch.equal(p, results[0][0]) and torch.equal(v, results[0][1])
+
+
+def test_a_step_is_seen_by_autograd(metis_lib):
+    """A parameter saved for a backward pass and then stepped: the pass is refused, as with torch's own."""
+    from spectral_quantized_gemm_b200.optim import AdamW
+    p = torch.nn.Parameter(torch.ones(8, device="cuda"))
+    opt = AdamW([p])
+    for _ in range(3):
+        loss = (p * p).sum()
+        p.grad = torch.ones_like(p)
+        opt.step()
+        with pytest.raises(RuntimeError):
+            loss.backward()
+
+
 def test_more_than_two_to_the_31_elements(metis_lib):
     from spectral_quantized_gemm_b200.optim import AdamW
     n = 2 ** 31 + 300

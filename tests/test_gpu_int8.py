@@ -61,6 +61,20 @@ def test_quantize_matches_the_oracle(ctx, shape, dtype, kind):
     assert ctx.poll_device_status() == 0
 
 
+@pytest.mark.parametrize("shape", [(1300, 1030), (600, 4100), (610, 8200), (600, 12000), (33, 33000)])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_quantize_large_matches_the_oracle(ctx, shape, dtype):
+    """Row lengths of every group size, and beyond what a group holds."""
+    M = _matrix(*shape, dtype, 1).cuda()
+    row, col = ctx.new_int8(*shape), ctx.new_int8(*shape[::-1])
+    ctx.quantize_int8(M, rowwise=row, colwise=col)
+    _check_quantized(row, M)
+    _check_quantized(col, M.t())
+    alone = ctx.new_int8(*shape)
+    ctx.quantize_int8(M, rowwise=alone)
+    assert torch.equal(alone.codes, row.codes) and torch.equal(alone.scales, row.scales)
+
+
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
 def test_quantize_reads_strided_rows_and_leaves_the_rest(ctx, metis_lib, dtype):
     base = _matrix(70, 411, dtype, 1).cuda()
@@ -351,6 +365,146 @@ def test_layer_broadcast_gradient_and_shared_weight(metis_lib):
     layer.weight.grad = None
     (layer(x).sum() + layer(x).sum()).backward()
     assert torch.equal(layer.weight.grad, once + once)
+
+
+@pytest.mark.parametrize("reduce", ["rows", "columns"])
+def test_layer_gradient_expanded_along_one_dimension(metis_lib, reduce):
+    """A mean over rows or columns hands the layer a gradient with a stride of 0."""
+    layer = _layer(64, 40, 21)
+    x = _matrix(24, 64, torch.bfloat16, 22).cuda().requires_grad_(True)
+    w = torch.randn(40 if reduce == "rows" else 24, device="cuda", generator=torch.Generator("cuda").manual_seed(0)).bfloat16()
+    (layer(x).sum(0 if reduce == "rows" else 1) * w).sum().backward()
+    dy = w.expand(24, 40) if reduce == "rows" else w[:, None].expand(24, 40)
+    _, dx, dw = _formula(_np(x), _np(layer.weight), _np(dy))
+    assert torch.equal(x.grad.cpu(), torch.from_numpy(dx).bfloat16())
+    assert torch.equal(layer.weight.grad.cpu(), torch.from_numpy(dw))
+
+
+def test_layer_on_expanded_and_padded_inputs(metis_lib):
+    layer = _layer(64, 40, 23)
+    row = _matrix(1, 64, torch.bfloat16, 24).cuda()
+    with torch.no_grad():
+        want = layer(row.expand(17, 64).contiguous())
+        assert torch.equal(layer(row.expand(17, 64)), want)
+        wide = torch.full((17, 100), 9.0, dtype=torch.bfloat16, device="cuda")
+        wide[:, 3:67] = row
+        assert torch.equal(layer(wide[:, 3:67]), want)
+        layer.freeze()
+        assert torch.equal(layer(row.expand(17, 64)), want)
+
+
+def test_layer_pass_captured_and_replayed(metis_lib):
+    layer = _layer(256, 136, 25)
+    x = torch.zeros(128, 256, dtype=torch.bfloat16, device="cuda", requires_grad=True)
+    dy = torch.zeros(128, 136, dtype=torch.bfloat16, device="cuda")
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        torch.autograd.grad(layer(x), (x, layer.weight), dy)
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        y = layer(x)
+        dx, dw = torch.autograd.grad(y, (x, layer.weight), dy)
+    for seed in range(3):
+        with torch.no_grad():
+            x.copy_(_matrix(128, 256, torch.bfloat16, 50 + seed))
+            dy.copy_(_matrix(128, 136, torch.bfloat16, 60 + seed))
+            layer.weight.mul_(0.75)
+        graph.replay()
+        torch.cuda.synchronize()
+        wy, wdx, wdw = _formula(_np(x), _np(layer.weight), _np(dy))
+        assert torch.equal(y.detach().cpu(), torch.from_numpy(wy).bfloat16())
+        assert torch.equal(dx.cpu(), torch.from_numpy(wdx).bfloat16())
+        assert torch.equal(dw.cpu(), torch.from_numpy(wdw))
+
+
+def test_layer_copies_and_casts(metis_lib):
+    import copy
+    import pickle
+    layer = _layer(64, 40, 26).freeze()
+    x = _matrix(5, 64, torch.bfloat16, 27).cuda()
+    with torch.no_grad():
+        want = layer(x)
+        for other in (copy.deepcopy(layer), pickle.loads(pickle.dumps(layer))):
+            assert other._frozen is None and torch.equal(other(x), want)
+        assert torch.equal(layer(x), want)
+        half = copy.deepcopy(layer).freeze().bfloat16()
+        with pytest.raises(RuntimeError):
+            half(x)
+        assert torch.equal(half.freeze()(x), half.unfreeze()(x))
+
+
+def test_two_threads_and_two_streams(metis_lib):
+    """Layers of one device share a context; passes from two threads on their own streams do not mix."""
+    import threading
+    layers = [_layer(256, 128, 30), _layer(128, 320, 31)]
+    xs = [_matrix(64, 256, torch.bfloat16, 32).cuda(), _matrix(96, 128, torch.bfloat16, 33).cuda()]
+    want = [layer(x).detach() for layer, x in zip(layers, xs)]
+    torch.cuda.synchronize()
+    bad = []
+
+    def work(i):
+        with torch.cuda.stream(torch.cuda.Stream()):
+            for _ in range(30):
+                x = xs[i].clone().requires_grad_(True)
+                y = layers[i](x)
+                y.sum().backward()
+                torch.cuda.current_stream().synchronize()
+                if not torch.equal(y.detach(), want[i]):
+                    bad.append(i)
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in (0, 1)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not bad
+
+
+def test_layer_call_refusals(ctx, metis_lib):
+    from spectral_quantized_gemm_b200.int8_linear import _buffers
+    dev = torch.device("cuda", 0)
+    X, W = torch.zeros(8, 32, device=dev), torch.zeros(32, 16, device=dev)
+    Y, D = torch.zeros(8, 16, device=dev), torch.zeros(8, 16, device=dev)
+    keep, (xr, wc, xc, wr, dr, dc) = _buffers(dev, ((8, 32, False), (16, 32, True), (32, 8, True), (32, 16, False), (8, 16, False), (16, 8, True)))
+
+    def status(call):
+        with pytest.raises(metis_lib.MetisError) as e:
+            call()
+        return e.value.status
+
+    ctx.int8_linear_fwd(X, W, Y, xr, wc, Xcol=xc, Wrow=wr)
+    assert status(lambda: ctx.int8_linear_fwd(X, W, Y, None, wc)) == 1
+    assert status(lambda: ctx.int8_linear_fwd(X, W, Y, xr, wr)) in (1, 2)                     # no scratch, wrong shape
+    assert status(lambda: ctx.int8_linear_fwd(X, W[:16], Y, xr, wc)) == 2
+    assert status(lambda: ctx.int8_linear_fwd(X, W, Y, xr, wc, Xcol=dr)) in (1, 2)
+    assert status(lambda: ctx.int8_linear_bwd(D, Drow=dr, Dcol=dc, Xcol=xc, Wrow=wr)) == 1    # nothing asked for
+    dX, dW = torch.zeros(8, 32, device=dev), torch.zeros(32, 16, device=dev)
+    assert status(lambda: ctx.int8_linear_bwd(D, Dcol=dc, Xcol=xc, dX=dX)) == 1
+    assert status(lambda: ctx.int8_linear_bwd(D, Drow=dr, Wrow=wr, dW=dW)) == 1
+    for call in (lambda: ctx.int8_linear_fwd(X, W, Y[:4], xr, wc), lambda: ctx.int8_linear_fwd(X.cpu(), W, Y, xr, wc),
+                 lambda: ctx.int8_linear_bwd(D, Drow=dr, Wrow=wr, dX=dX[:, :16]),
+                 lambda: ctx.int8_linear_bwd(D, Dcol=dc, Xcol=xc, dW=dW.bfloat16())):
+        with pytest.raises(ValueError):
+            call()
+    ctx.int8_linear_bwd(D, Drow=dr, Dcol=dc, Xcol=xc, Wrow=wr, dX=dX, dW=dW)
+    assert ctx.poll_device_status() == 0 and not dX.any() and not dW.any()
+    no_scratch = metis_lib.Int8(32, 8)
+    assert metis_lib._quant_i8(ctx._h, X.data_ptr(), 8, 32, 32, 0, None, metis_lib.ctypes.byref(no_scratch.struct)) == 1
+
+
+def test_frozen_layer_notices_the_optimizer(metis_lib):
+    from spectral_quantized_gemm_b200.optim import AdamW
+    layer = _layer(64, 40, 28).freeze()
+    opt = AdamW(layer.parameters(), lr=0.1)
+    x = _matrix(5, 64, torch.bfloat16, 29).cuda()
+    for _ in range(3):                                     # a first step, and steps from a plan
+        layer.freeze()
+        layer(x).sum().backward()
+        opt.step()
+        with torch.no_grad(), pytest.raises(RuntimeError):
+            layer(x)
 
 
 def test_frozen_layer_serves_and_notices_a_changed_weight(metis_lib):
