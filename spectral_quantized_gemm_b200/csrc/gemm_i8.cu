@@ -13,8 +13,8 @@
 //   warp 1      tensor-memory owner and MMA issuer (one thread)
 //   warps 2..5  epilogue
 // Channels on the lanes suit few tokens (no lane idles) and let the staged sums be written
-// and read without bank conflicts; at 512 x 768 x 2304 the other way round took 7.5 us, this
-// one 7.1.
+// and read without bank conflicts; at 512 x 768 x 2304 the other way round took 7.5 us where this
+// one, with the same tile and no more changes, took 7.1.
 //
 // gemm_i8_pair_kernel: large products.  A cluster of two CTAs computes 256 x 256 tiles with
 // cta_group::2 MMAs (each CTA loads 128 rows of A and 128 of B for every 128 K elements),
@@ -58,7 +58,7 @@ struct Cfg {
   static constexpr int STAGE_BYTES = A_BYTES + B_BYTES;
   static constexpr int TMEM_COLS = BN < 32 ? 32 : BN;
   // Two or three CTAs fit an SM.  (Rings of 8 or 12 stages for a CTA that has its SM to itself were
-  // no faster: 512 x 768 x 2304 7.1 us against 6.5.)
+  // no faster: 512 x 768 x 2304 7.1 us where 4 stages took 6.5.)
   static constexpr int STAGES = SPLIT || BN == 32 ? 3 : 4;
   static constexpr int PER_SM = BN == 16 || (BN == 32 && !SPLIT) ? 3 : 2;
   static constexpr int PITCH = 128 + 4;                // words of a staged row of sums
@@ -616,17 +616,17 @@ metis_status launch_gemm_i8(metis_ctx* ctx, const metis_int8* A, const metis_int
   const int bn = prm.p <= 16 ? 16 : prm.p <= 32 ? 32 : 64;
   const int64_t tiles = ((prm.q + 127) / 128) * ((prm.p + bn - 1) / bn);
   // Tile kernel or CTA pairs.  While the tiles of the former fit the SMs at once (two each) it is
-  // ahead: 512 x 4096 x 4096 16.7 us against 19.0, 1024 x 1024 x 1024 7.1 against 9.9; with a
-  // second wave it is behind: 2048 x 512 x 2048 13.3 against 10.3.  Up to 128 rows of A leave half
+  // ahead: 512 x 4096 x 4096 15.5 us against 18.5, 1024 x 1024 x 1024 6.1 against 9.2; with a
+  // second wave it is behind: 2048 x 512 x 2048 11.4 against 9.8.  Up to 128 rows of A leave half
   // of a pair's tile empty.
   if (prm.p > 128 && tiles > 2 * ctx->sm_count) return launch_pair(ctx, A, B, prm);
   // Shares of K.  Up to 16 tokens a join costs little, and more CTAs stream the weight faster
-  // (1 x 4096 x 4096: 12.8 us in one share, 8.2 in eight; 1 x 4096 x 14336: 15.2, 13.8 in three,
-  // 17.3 in four, which no longer fit the SMs three to each).  With 32 or 64 the join moves more:
-  // one CTA an SM and eight blocks of K each (40 x 4096 x 4096: 14.1, 10.3 in four, 12.6 in eight;
-  // 512 x 2304 x 768: 9.6, 9.1 in two, 10.0 in three).
+  // (1 x 4096 x 4096: 11.9 us in one share, 6.8 in eight; 1 x 768 x 2304: 3.8, 3.3 in six;
+  // 1 x 4096 x 14336: 14.2, 12.6 in three, 16.6 in four, which no longer fit the SMs three to
+  // each).  With 32 or 64 the join moves more: one CTA an SM and eight blocks of K each (40 x 4096 x
+  // 4096: 13.1, 9.2 in four, 10.2 in eight; 512 x 2304 x 768: 8.8, 8.0 in two, 9.5 in three).
   const int64_t room = (bn == 16 ? ctx->sm_count * 27 / 10 : ctx->sm_count) / tiles;
-  const int splits = (int)std::max<int64_t>(1, std::min<int64_t>({kMaxSplits, room, prm.k_tiles / (bn == 16 ? 4 : 8)}));
+  const int splits = (int)std::max<int64_t>(1, std::min<int64_t>({kMaxSplits, room, prm.k_tiles / (bn == 16 ? 1 : 8)}));
   auto launch = [&](auto zero) {
     using OUT = decltype(zero);
 #define METIS_TILE(BN) \
