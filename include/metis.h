@@ -356,7 +356,7 @@ typedef struct {
  * dtype METIS_OUT_F32 or METIS_OUT_BF16, aligned to its element), round to nearest:
  *   rowwise (nullable): outer = rows, inner = cols, a scale for each row (token)
  *   colwise (nullable): outer = cols, inner = rows, a scale for each column (channel); M^T;
- *     needs its scratch
+ *     needs its scratch; both together: each its own memory
  * For a line with amax = max |x| over its finite entries and a = max(amax, 127 * 2^-126):
  * scale = fp32(a / 127), code = 127 x / a rounded to the nearest integer, ties to even,
  * decided on the exact quotient.  A line of zeros has zero codes.  NaN gives code 0, an
@@ -403,6 +403,7 @@ typedef struct {
  *   dX (nullable) = Drow Wrow^T (l x m, type dx_dtype), Drow <- Q(D) by tokens (l x n);
  *   dW (nullable) = Xcol Dcol^T (m x n fp32), Dcol <- Q(D) by output channels (n x l, needs scratch).
  * The same results as the calls above one by one.  l, m, n <= 131071 where they are contracted.
+ * Outputs must not overlap; scratches of Xcol and Wcol that do are refused (ERR_ARG).
  */
 metis_status metis_int8_linear_fwd(metis_ctx* ctx, const metis_dense* X, const metis_dense* W, metis_int8* Xrow,
                                    metis_int8* Xcol, metis_int8* Wrow, metis_int8* Wcol, void* Y, int64_t ldy,

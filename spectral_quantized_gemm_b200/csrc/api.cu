@@ -633,6 +633,8 @@ metis_status check_quantize_int8(metis_ctx* ctx, const void* M, int64_t rows, in
     return fail(ctx, METIS_ERR_SHAPE, "rowwise: expected outer x inner = rows x cols");
   if (colwise && (colwise->outer != cols || colwise->inner != rows))
     return fail(ctx, METIS_ERR_SHAPE, "colwise: expected outer x inner = cols x rows");
+  if (rowwise && colwise && (rowwise->codes == colwise->codes || rowwise->scales == colwise->scales))
+    return fail(ctx, METIS_ERR_ARG, "rowwise and colwise need codes and scales of their own");
   return METIS_OK;
 }
 
@@ -738,6 +740,10 @@ metis_status metis_int8_linear_fwd(metis_ctx* ctx, const metis_dense* X, const m
     if (s != METIS_OK || (s = check_quantize_int8(ctx, W->data, W->rows, W->cols, W->ld, W->dtype, Wrow, Wcol)) != METIS_OK ||
         (s = check_gemm_int8(ctx, Xrow, Wcol, Y, ldy, y_dtype)) != METIS_OK)
       return s;
+    // both are cleared at once, so one would find the other's maxima
+    if (Xcol && Xcol->scratch < Wcol->scratch + METIS_INT8_SCRATCH * Wcol->outer &&
+        Wcol->scratch < Xcol->scratch + METIS_INT8_SCRATCH * Xcol->outer)
+      return fail(ctx, METIS_ERR_ARG, "Xcol and Wcol need a scratch each");
     if ((s = clear_scratch(ctx, Wcol, Xcol)) != METIS_OK || (s = quantize_int8(ctx, X, Xrow, Xcol)) != METIS_OK ||
         (s = quantize_int8(ctx, W, Wrow, Wcol)) != METIS_OK)
       return s;

@@ -217,6 +217,8 @@ def test_refusals(ctx, metis_lib):
     assert status(lambda: ctx.quantize_int8(X)) == 1
     assert status(lambda: ctx.quantize_int8(X, rowwise=t)) == 2
     assert status(lambda: ctx.quantize_int8(X, colwise=q)) == 2
+    square = ctx.new_int8(32, 32)
+    assert status(lambda: ctx.quantize_int8(torch.zeros(32, 32, device="cuda"), rowwise=square, colwise=square)) == 1
     odd = metis_lib.Int8(4, 24, codes=torch.zeros(4, 24, dtype=torch.int8, device="cuda"))
     assert status(lambda: ctx.quantize_int8(X[:, :24], rowwise=odd)) == 3             # row stride 24
     shifted = metis_lib.Int8(4, 32, codes=torch.zeros(4, 48, dtype=torch.int8, device="cuda")[:, 8:40])
@@ -480,6 +482,10 @@ def test_layer_call_refusals(ctx, metis_lib):
     assert status(lambda: ctx.int8_linear_fwd(X, W[:16], Y, xr, wc)) == 2
     assert status(lambda: ctx.int8_linear_fwd(X, W, Y, xr, wc, Xcol=dr)) in (1, 2)
     assert status(lambda: ctx.int8_linear_bwd(D, Drow=dr, Dcol=dc, Xcol=xc, Wrow=wr)) == 1    # nothing asked for
+    wide = metis_lib.Int8Struct(xc.codes, xc.scales, 32, 8, xc.ld, wc.scratch)                # Wcol's scratch
+    assert status(lambda: ctx.int8_linear_fwd(X, W, Y, xr, wc, Xcol=wide, Wrow=wr)) == 1
+    wide.scratch = wc.scratch + 4 * 9 * 16 - 4                                                # its last word
+    assert status(lambda: ctx.int8_linear_fwd(X, W, Y, xr, wc, Xcol=wide, Wrow=wr)) == 1
     dX, dW = torch.zeros(8, 32, device=dev), torch.zeros(32, 16, device=dev)
     assert status(lambda: ctx.int8_linear_bwd(D, Dcol=dc, Xcol=xc, dX=dX)) == 1
     assert status(lambda: ctx.int8_linear_bwd(D, Drow=dr, Wrow=wr, dW=dW)) == 1
