@@ -235,7 +235,7 @@ class AdamW(torch.optim.Optimizer):
                 state.update(self._new_state(p, bits))
             m, v = state["exp_avg"], state["exp_avg_sq"]
             if not (m.dtype is state_dtype and v.dtype is state_dtype and m.numel() == n and v.numel() == n and
-                    m.is_cuda and v.is_cuda and
+                    m.device == v.device == p.device and
                     (m.is_contiguous() and v.is_contiguous() if plain else m.stride() == p.stride() == v.stride())):
                 raise ValueError(f"a state does not fit its parameter with state_bits={bits}")
             e, f = m, v
@@ -243,7 +243,7 @@ class AdamW(torch.optim.Optimizer):
                 e, f = state["exp_avg_exponent"], state["exp_avg_sq_exponent"]
                 blocks = -(-n // BLOCK)
                 if not (e.dtype is state_dtype and f.dtype is state_dtype and e.numel() == blocks and f.numel() == blocks and
-                        e.is_contiguous() and f.is_contiguous() and e.is_cuda and f.is_cuda):
+                        e.is_contiguous() and f.is_contiguous() and e.device == f.device == p.device):
                     raise ValueError("a state's exponents do not fit its parameter")
             if not capturable:
                 t = int(state["step"])
@@ -254,6 +254,9 @@ class AdamW(torch.optim.Optimizer):
             # the last word holds the struct's two 32-bit fields, dtype and id
             rows.extend((p.data_ptr(), g.data_ptr(), m.data_ptr(), v.data_ptr(), e.data_ptr(), f.data_ptr(), n,
                          (OUT_F32 if dtype is torch.float32 else OUT_BF16) | (first + i) << 32))
+        taken = [p.data_ptr() for _, p, _ in todo if p.numel()]
+        if len(set(taken)) < len(taken):
+            raise ValueError("two parameters of a group lie at the same address")
         if capturable:
             if len(calls) > 1:
                 raise ValueError("the parameters of a capturable group must be on one device")

@@ -435,11 +435,16 @@ def test_refusals(metis_lib):
     opt.step()
     good = dict(opt.state[p])
     for name, bad in (("exp_avg", good["exp_avg"].float()), ("exp_avg", good["exp_avg"][:200]),
-                      ("exp_avg_sq_exponent", good["exp_avg_sq_exponent"][:2]), ("exp_avg_exponent", good["exp_avg_exponent"].int())):
+                      ("exp_avg_sq_exponent", good["exp_avg_sq_exponent"][:2]), ("exp_avg_exponent", good["exp_avg_exponent"].int()),
+                      ("exp_avg_sq", good["exp_avg_sq"].cpu()), ("exp_avg_exponent", good["exp_avg_exponent"].cpu())):
         opt.state[p] = {**good, name: bad}
         with pytest.raises(ValueError):
             opt.step()
     opt.state[p] = good
+    twin = torch.nn.Parameter(p.detach())                  # another parameter on the same memory
+    twin.grad = p.grad.clone()
+    with pytest.raises(ValueError):
+        AdamW([p, twin], **HYPER).step()
     opt.param_groups[0]["state_bits"] = 32
     with pytest.raises(ValueError):
         opt.step()
