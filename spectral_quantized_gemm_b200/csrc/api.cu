@@ -653,7 +653,7 @@ metis_status check_gemm_int8(metis_ctx* ctx, const metis_int8* A, const metis_in
 }
 
 metis_status clear_scratch(metis_ctx* ctx, const metis_int8* a, const metis_int8* b) {
-  return check_cuda(ctx, clear_int8_scratch(a, b, ctx->stream), "int8 scratch");
+  return check_cuda(ctx, clear_int8_scratch(a, b, ctx->sm_count, ctx->stream), "int8 scratch");
 }
 // The scratch of col is clear.
 metis_status quantize_int8(metis_ctx* ctx, const metis_dense* M, const metis_int8* row, const metis_int8* col) {

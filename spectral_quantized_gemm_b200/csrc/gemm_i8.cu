@@ -196,7 +196,7 @@ __global__ void __launch_bounds__(kThreads)
     const int t = (int)threadIdx.x - 64;
     const int64_t j = (int64_t)lb * 128 + t;
     if (!p.early) tc::grid_dependency_wait();
-    sb[t] = j < p.q ? p.sb[j] : 0.0f;
+    sb[t] = j < p.q ? __ldcg(&p.sb[j]) : 0.0f;   // from L2: no cache of this SM can hold an older one
     if (p.early) tc::grid_dependency_wait();
     tc::grid_launch_dependents();
     if (t < BN) sa[t] = (int64_t)cb * BN + t < p.p ? p.sa[(int64_t)cb * BN + t] : 0.0f;

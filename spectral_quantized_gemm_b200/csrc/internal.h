@@ -201,7 +201,7 @@ metis_status run_lora_realign(metis_ctx* ctx, float* W, int64_t m, int64_t n, in
 
 // ---- quantize_i8.cu ----
 // Zeroes the scratch of up to two column-wise outputs (each nullable), which the quantizer expects.
-cudaError_t clear_int8_scratch(const metis_int8* a, const metis_int8* b, cudaStream_t st);
+cudaError_t clear_int8_scratch(const metis_int8* a, const metis_int8* b, int sm_count, cudaStream_t st);
 // Codes and scales of the rows (row, nullable) and of the columns (col, nullable, transposed).
 cudaError_t launch_quantize_i8(const void* M, bool bf16, int64_t rows, int64_t cols, int64_t ld, const metis_int8* row,
                                const metis_int8* col, uint32_t* status, int sm_count, cudaStream_t st);

@@ -23,7 +23,6 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
-#include <utility>
 
 #include "device_common.cuh"
 #include "internal.h"
@@ -461,6 +460,14 @@ __global__ void __launch_bounds__(kThreads, 4) quantize_i8_cols_kernel(const T* 
   }
 }
 
+// Zeroes two stretches of words.  A kernel, not a memset: the next one is launched under it.
+__global__ void __launch_bounds__(kThreads) clear_i8_scratch_kernel(uint32_t* a, int64_t na, uint32_t* b, int64_t nb) {
+  tc::grid_dependency_wait();
+  tc::grid_launch_dependents();
+  for (int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x; i < na + nb; i += (int64_t)gridDim.x * kThreads)
+    *(i < na ? a + i : b + (i - na)) = 0;
+}
+
 // ---------------------------------------------------------------- launches
 // All kernels here are launched so that they may start under the tail of the one before.
 template <typename T, int GROUP, int HELD, bool TOPS>
@@ -528,17 +535,11 @@ cudaError_t run_quantize(const T* M, int64_t rows, int64_t cols, int64_t ld, con
 
 }  // namespace
 
-cudaError_t clear_int8_scratch(const metis_int8* a, const metis_int8* b, cudaStream_t st) {
-  if (a && b && b->scratch + METIS_INT8_SCRATCH * b->outer == a->scratch) std::swap(a, b);
-  cudaError_t e = cudaSuccess;
-  size_t words = a ? (size_t)METIS_INT8_SCRATCH * a->outer : 0;
-  if (a && b && a->scratch + words == b->scratch) {   // side by side: one fill
-    words += (size_t)METIS_INT8_SCRATCH * b->outer;
-    b = nullptr;
-  }
-  if (a) e = cudaMemsetAsync(a->scratch, 0, words * 4, st);
-  if (b && e == cudaSuccess) e = cudaMemsetAsync(b->scratch, 0, (size_t)METIS_INT8_SCRATCH * b->outer * 4, st);
-  return e;
+cudaError_t clear_int8_scratch(const metis_int8* a, const metis_int8* b, int sm_count, cudaStream_t st) {
+  const int64_t na = a ? (int64_t)METIS_INT8_SCRATCH * a->outer : 0, nb = b ? (int64_t)METIS_INT8_SCRATCH * b->outer : 0;
+  if (na + nb == 0) return cudaSuccess;
+  const int64_t blocks = std::min<int64_t>((na + nb + kThreads - 1) / kThreads, 2 * (int64_t)sm_count);
+  return launch_early(clear_i8_scratch_kernel, blocks, kThreads, 0, st, a ? a->scratch : nullptr, na, b ? b->scratch : nullptr, nb);
 }
 
 cudaError_t launch_quantize_i8(const void* M, bool bf16, int64_t rows, int64_t cols, int64_t ld, const metis_int8* row,
