@@ -367,7 +367,7 @@ __global__ void __launch_bounds__(512) quantize_i8_long_rows_kernel(const T* __r
 }
 
 // ---------------------------------------------------------------- columns
-// The codes of the columns from their maxima: a tile of 128 bytes of 256 rows goes to shared
+// The codes of the columns from their maxima: a tile of 128 bytes of ROWS rows goes to shared
 // memory, all of it on its way at once (cp.async), also under the tail of the kernel that makes
 // the maxima.  Then a thread takes a word of a row (two columns bf16, one fp32) in 16
 // consecutive rows, so its codes are 16 bytes of a column each; the lanes of a warp are 4 words
@@ -377,7 +377,7 @@ __global__ void __launch_bounds__(512) quantize_i8_long_rows_kernel(const T* __r
 //   (One reading instead of two, by clusters that keep strips of columns in shared memory while
 // their maxima are joined, took 36 us or more at 8192 x 4096 bf16 in all forms tried: a block
 // waited most of its time for the join.)
-constexpr int kPiece = 16, kTileRows = 256, kRowBytes = 128;
+constexpr int kPiece = 16, kRowBytes = 128;
 constexpr int kPieceBytes = kPiece * kRowBytes + 16;
 
 __device__ __forceinline__ void copy_async16(void* dst, const void* src) {
@@ -385,16 +385,16 @@ __device__ __forceinline__ void copy_async16(void* dst, const void* src) {
 }
 __device__ __forceinline__ void copy_async_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 
-template <typename T>
+template <typename T, int ROWS>
 __global__ void __launch_bounds__(kThreads, 4) quantize_i8_cols_kernel(const T* __restrict__ M, int64_t rows, int64_t cols,
                                                                        int64_t ld, int8_t* __restrict__ codes, int64_t ldq,
                                                                        float* __restrict__ scales, const uint32_t* tops,
                                                                        const uint32_t* marks) {
   constexpr int COLS = kRowBytes / (int)sizeof(T), PER_WORD = 4 / (int)sizeof(T);
-  __shared__ __align__(16) uint8_t data[kTileRows / kPiece * kPieceBytes];
+  __shared__ __align__(16) uint8_t data[ROWS / kPiece * kPieceBytes];
   const int64_t strips = (cols + COLS - 1) / COLS, c0 = (blockIdx.x % strips) * COLS;
-  const int64_t tile = (rows + kTileRows - 1) / kTileRows - 1 - blockIdx.x / strips, r0 = tile * kTileRows;
-  const int n = (int)min((int64_t)kTileRows, rows - r0);
+  const int64_t tile = (rows + ROWS - 1) / ROWS - 1 - blockIdx.x / strips, r0 = tile * ROWS;
+  const int n = (int)min((int64_t)ROWS, rows - r0);
   const bool aligned = ((reinterpret_cast<uintptr_t>(M) | (uintptr_t)(ld * (int64_t)sizeof(T))) & 15u) == 0;
   if (aligned && c0 + COLS <= cols) {
     const int chunk = threadIdx.x & 7;
@@ -427,7 +427,7 @@ __global__ void __launch_bounds__(kThreads, 4) quantize_i8_cols_kernel(const T* 
   copy_async_wait_all();
   __syncthreads();
 #pragma unroll 1
-  for (int piece = lane >> 2; piece < kTileRows / kPiece; piece += 8) {
+  for (int piece = lane >> 2; piece < ROWS / kPiece; piece += 8) {
     const int left = n - piece * kPiece;
     if (left <= 0) break;
     const uint32_t* w = reinterpret_cast<const uint32_t*>(data + piece * kPieceBytes) + word;
@@ -529,8 +529,16 @@ cudaError_t run_quantize(const T* M, int64_t rows, int64_t cols, int64_t ld, con
   }
   if (e != cudaSuccess) return e;
   constexpr int COLS = kRowBytes / (int)sizeof(T);
-  return launch_early(quantize_i8_cols_kernel<T>, (cols + COLS - 1) / COLS * ((rows + kTileRows - 1) / kTileRows), kThreads, 0, st,
-                      M, rows, cols, ld, col->codes, col->ld, col->scales, (const uint32_t*)tops, (const uint32_t*)marks);
+  const int64_t strips = (cols + COLS - 1) / COLS;
+  auto launch = [&](auto kern, int64_t tile) {
+    return launch_early(kern, strips * ((rows + tile - 1) / tile), kThreads, 0, st, M, rows, cols, ld, col->codes, col->ld,
+                        col->scales, (const uint32_t*)tops, (const uint32_t*)marks);
+  };
+  // Rows of a tile: 256, or half that where there would be fewer than two blocks for an SM.  Both
+  // orientations, 128 against 256: 1001 x 1333 bf16 9.6 us, 14.2; 512 x 2304 8.6, 10.3; 2048 x 2048 11.2,
+  // 11.9; 4096 x 2048 15.5, 14.9; 8192 x 4096 47.7, 42.8.
+  if (strips * ((rows + 255) / 256) < 2 * (int64_t)sm_count) return launch(quantize_i8_cols_kernel<T, 128>, 128);
+  return launch(quantize_i8_cols_kernel<T, 256>, 256);
 }
 
 }  // namespace
