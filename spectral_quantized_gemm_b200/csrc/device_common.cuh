@@ -178,6 +178,31 @@ __device__ __forceinline__ float pow2_ceil(float t) {
   return __uint_as_float((e + 1) << 23);
 }
 
+// Two fp32 numbers in a 64-bit register and operations on both in one instruction, each rounded to
+// nearest as the single one.
+struct Pair {
+  uint64_t v;
+  __device__ __forceinline__ explicit Pair(uint64_t bits) : v(bits) {}
+  __device__ __forceinline__ Pair(float lo, float hi) { asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(lo), "f"(hi)); }
+  __device__ __forceinline__ explicit Pair(float both) : Pair(both, both) {}
+  __device__ __forceinline__ void get(float& lo, float& hi) const { asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v)); }
+};
+__device__ __forceinline__ Pair operator*(Pair a, Pair b) {
+  uint64_t d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a.v), "l"(b.v));
+  return Pair(d);
+}
+__device__ __forceinline__ Pair operator+(Pair a, Pair b) {
+  uint64_t d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a.v), "l"(b.v));
+  return Pair(d);
+}
+__device__ __forceinline__ Pair fma2(Pair a, Pair b, Pair c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a.v), "l"(b.v), "l"(c.v));
+  return Pair(d);
+}
+
 __device__ __forceinline__ void raise_status(uint32_t* status, uint32_t bits) {
   if (status) atomicOr(status, bits);
 }

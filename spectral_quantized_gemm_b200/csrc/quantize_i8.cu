@@ -68,16 +68,23 @@ __device__ __noinline__ int code_exact(float x, float a, float inv) {
   return x < 0.0f ? -c : c;
 }
 
-// The code in the low byte, for a line that needs no fp64 comparison; fp32: near a border it is
-// open and `near` is raised.
+// The codes of two elements in the low bytes, for a line that needs no fp64 comparison; fp32: `border`
+// becomes the largest distance from an integer, near a half the code is open.
 template <typename T>
-__device__ __forceinline__ uint32_t code_bits(float x, const LineScale& s, bool& near) {
-  const float y = __fmaf_rn(x, s.inv, __fmul_rn(x, s.lo));
-  const float t = __fadd_rn(y, 12582912.0f);
-  if constexpr (sizeof(T) == 4) near |= fabsf(__fsub_rn(y, __fsub_rn(t, 12582912.0f))) > 0.49996f;
-  return __float_as_uint(t);
+__device__ __forceinline__ void code_bits(float x0, float x1, const LineScale& s, uint32_t& b0, uint32_t& b1, float& border) {
+  const Pair x(x0, x1), magic(12582912.0f);
+  const Pair y = fma2(x, Pair(s.inv), x * Pair(s.lo)), t = y + magic;
+  float t0, t1;
+  t.get(t0, t1);
+  b0 = __float_as_uint(t0);
+  b1 = __float_as_uint(t1);
+  if constexpr (sizeof(T) == 4) {
+    float d0, d1;
+    fma2(t + Pair(-12582912.0f), Pair(-1.0f), y).get(d0, d1);
+    border = fmaxf(border, fmaxf(fabsf(d0), fabsf(d1)));
+  }
 }
-// The same with the comparison.
+// The code of one element with the comparison.
 __device__ __forceinline__ uint32_t code_at_border(float x, const LineScale& s) {
   const float y = __fmaf_rn(x, s.inv, __fmul_rn(x, s.lo));
   const float t = __fadd_rn(y, 12582912.0f);
@@ -161,10 +168,11 @@ __device__ __noinline__ uint32_t four_open(float x0, float x1, float x2, float x
 }
 template <typename T>
 __device__ __forceinline__ uint32_t four_codes(float x0, float x1, float x2, float x3, const LineScale& s) {
-  bool near = s.a < 0.0f;
-  const uint32_t b0 = code_bits<T>(x0, s, near), b1 = code_bits<T>(x1, s, near), b2 = code_bits<T>(x2, s, near),
-                 b3 = code_bits<T>(x3, s, near);
-  if (near) return four_open(x0, x1, x2, x3, s.a, s.inv, s.lo);
+  uint32_t b0, b1, b2, b3;
+  float border = 0.0f;
+  code_bits<T>(x0, x1, s, b0, b1, border);
+  code_bits<T>(x2, x3, s, b2, b3, border);
+  if (s.a < 0.0f || border > 0.49996f) return four_open(x0, x1, x2, x3, s.a, s.inv, s.lo);
   return pack4(b0, b1, b2, b3);
 }
 template <typename T>
