@@ -313,23 +313,22 @@ __device__ __forceinline__ bool step_block(Block4& x, const Step& s, double b1, 
   const bool usual = x.tm <= 14 && x.tv <= 30;
   // the coefficients of the codes as they are: exact, the decoding factors are powers of two
   const float dm = power2f(min(x.tm, 14) + 112), dv = power2f(min(x.tv, 30) + 96);
-  const float b1m = s.b1 * dm, b1m_low = s.b1_low * dm, b2v = s.b2 * dv;
+  const Pair b1m(s.b1 * dm), b1m_low(-s.b1_low * dm), b2v(s.b2 * dv);
   float ym[4], yv[4];
   float hm = 0.0f;
   uint32_t hv = 0;
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
+  for (int j = 0; j < 4; j += 2) {
     // code j in the top byte, then its sign and magnitude in place
-    const int top = (int)__byte_perm(x.cm, 0u, (j << 12) | 0x0444u);
-    const float om = __uint_as_float((uint32_t)(top >> 4) & 0x87F00000u);
-    const float ov = __uint_as_float(__byte_perm(x.cv, 0u, (j << 12) | 0x0444u) >> 4);
-    const float g = x.g[j];
+    auto old_m = [&](int j) { return __uint_as_float((uint32_t)((int)__byte_perm(x.cm, 0u, (j << 12) | 0x0444u) >> 4) & 0x87F00000u); };
+    auto old_v = [&](int j) { return __uint_as_float(__byte_perm(x.cv, 0u, (j << 12) | 0x0444u) >> 4); };
+    const Pair om(old_m(j), old_m(j + 1)), ov(old_v(j), old_v(j + 1)), g(x.g[j], x.g[j + 1]);
     // b1 m + (1 - b1) g: the first product exact within the sum (m has four bits, the coefficient
-    // twenty), the second with its remainder; two roundings of the sum, so two units
-    const float add = s.a1 * g;
-    const float rest = fmaf(b1m_low, om, fmaf(s.a1_low, g, fmaf(s.a1, g, -add)));
-    ym[j] = fmaf(b1m, om, add) + rest;
-    yv[j] = fmaf(b2v, ov, s.a2 * (g * g));   // five roundings: three units
+    // twenty), the second with its remainder (here negated); two roundings of the sum, so two units
+    const Pair add = Pair(s.a1) * g;
+    const Pair rest = fma2(b1m_low, om, fma2(Pair(-s.a1_low), g, fma2(Pair(-s.a1), g, add)));
+    fma2(rest, Pair(-1.0f), fma2(b1m, om, add)).get(ym[j], ym[j + 1]);
+    fma2(b2v, ov, Pair(s.a2) * (g * g)).get(yv[j], yv[j + 1]);   // five roundings: three units
   }
   if (!usual) {
 #pragma unroll
@@ -346,7 +345,16 @@ __device__ __forceinline__ bool step_block(Block4& x, const Step& s, double b1, 
   }
   if (!s.tiny) {
 #pragma unroll
-    for (int j = 0; j < 4; ++j) x.p[j] = stepped<false>(x.p[j], ym[j], yv[j], s);
+    for (int j = 0; j < 4; j += 2) {   // as stepped<false>
+      float r0, r1, q0, q1;
+      asm("sqrt.approx.ftz.f32 %0, %1;" : "=f"(r0) : "f"(yv[j]));
+      asm("sqrt.approx.ftz.f32 %0, %1;" : "=f"(r1) : "f"(yv[j + 1]));
+      fma2(Pair(r0, r1), Pair(s.rbc2), Pair(s.eps)).get(r0, r1);
+      asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(q0) : "f"(r0));
+      asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(q1) : "f"(r1));
+      const Pair q = Pair(q0, q1) * Pair(ym[j], ym[j + 1]);
+      fma2(Pair(-s.size), q, Pair(x.p[j], x.p[j + 1]) * Pair(s.decay)).get(x.p[j], x.p[j + 1]);
+    }
   } else {
 #pragma unroll
     for (int j = 0; j < 4; ++j) x.p[j] = stepped<true>(x.p[j], ym[j], yv[j], s);
