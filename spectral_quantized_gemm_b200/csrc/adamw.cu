@@ -137,7 +137,7 @@ __device__ __forceinline__ Words4 stream_words(const uint2 (&keys)[10], uint32_t
 // Four consecutive elements as they are in memory; unpacked where they are used, so that a load
 // ahead is not waited for.
 template <typename T>
-struct Four {
+struct __align__(4 * sizeof(T)) Four {
   uint32_t w[(int)sizeof(T)];
   __device__ __forceinline__ float get(int j) const {
     if constexpr (sizeof(T) == 4) return __uint_as_float(w[j]);
@@ -448,10 +448,32 @@ struct View {
   }
 };
 
+// What a block has on its way in shared memory: each thread copies its own elements of the next two state
+// blocks here and reads them back, so nothing but the copies is waited for.  Only fp32 to nearest, which
+// waited for memory with one state block ahead in registers (71 M elements 220 us, 200 with the ring;
+// four or six stages 202, 209).  The others are bound by their instructions, and these are more: fp32
+// stochastic 238 us, 240 with it; bf16 301, 318 stochastic, 260, 274 to nearest.
+template <typename T>
+struct Ring {
+  static constexpr int STAGES = 3;
+  Four<T> p[STAGES][kThreads], g[STAGES][kThreads];
+  uint32_t cm[STAGES][kThreads], cv[STAGES][kThreads];
+};
+template <typename T, int BITS, bool SR>
+constexpr bool kRing = BITS == 8 && sizeof(T) == 4 && !SR;
+template <int BYTES>
+__device__ __forceinline__ void copy_async(void* dst, const void* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(tc::smem_addr(dst)), "l"(src), "n"(BYTES) : "memory");
+}
+__device__ __forceinline__ void copy_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int PENDING>
+__device__ __forceinline__ void copy_async_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(PENDING) : "memory"); }
+
 // One chunk (elements base .. base + units * kUnit of a tensor).  Returns whether a gradient of the
 // thread is not finite.
 template <typename T, int BITS, bool SR, bool FAST, int CAP>
-__device__ __forceinline__ bool run_chunk(const Table<CAP>& tab, int which, int64_t base, const View<T, FAST>& a, const Step& s) {
+__device__ __forceinline__ bool run_chunk(const Table<CAP>& tab, int which, int64_t base, const View<T, FAST>& a, const Step& s,
+                                          Ring<T>* ring) {
   bool bad = false;
   const uint32_t tag = stream_tag(tab.id[which], kPurposeState, 0);
   if constexpr (BITS == 32) {
@@ -480,6 +502,7 @@ __device__ __forceinline__ bool run_chunk(const Table<CAP>& tab, int which, int6
       a.store(i, xp, SR, w);
     }
   } else {
+    constexpr bool AHEAD = FAST && kRing<T, BITS, SR>;
     uint8_t* m = static_cast<uint8_t*>(a.m);
     uint8_t* v = static_cast<uint8_t*>(a.v);
     uint8_t* me = tab.t[which].me;
@@ -491,10 +514,23 @@ __device__ __forceinline__ bool run_chunk(const Table<CAP>& tab, int which, int6
     const int64_t first = base + (int64_t)(threadIdx.x >> 5) * tab.units * kStateBlock;
     if (!a.in(first)) return false;
     const int blocks = FAST ? tab.units : (int)min((int64_t)tab.units, (a.n - first + kStateBlock - 1) / kStateBlock);
+    int64_t i = first + lane * 4;
+    auto fetch = [&](int u, int64_t e) {   // elements e on, of the warp's state block u
+      if (u < blocks) {
+        const int at = u % Ring<T>::STAGES;
+        copy_async<sizeof(Four<T>)>(&ring->p[at][threadIdx.x], a.p + e);
+        copy_async<sizeof(Four<T>)>(&ring->g[at][threadIdx.x], a.g + e);
+        copy_async<4>(&ring->cm[at][threadIdx.x], m + e);
+        copy_async<4>(&ring->cv[at][threadIdx.x], v + e);
+      }
+      copy_async_commit();
+    };
+    if constexpr (AHEAD)
+#pragma unroll
+      for (int u = 0; u < Ring<T>::STAGES - 1; ++u) fetch(u, i + u * kStateBlock);
     const int64_t blk = first / kStateBlock + lane;
     const int old_me = lane < blocks ? (int)me[blk] - 127 : 0, old_ve = lane < blocks ? (int)ve[blk] - 127 : 0;
     int new_me = 0, new_ve = 0;
-    int64_t i = first + lane * 4;
     struct {
       Four<T> p, g;
       uint32_t cm, cv;
@@ -505,8 +541,17 @@ __device__ __forceinline__ bool run_chunk(const Table<CAP>& tab, int which, int6
       next.cm = load_codes(m, i, FAST ? i + 4 : a.n, FAST || a.vec_s);
       next.cv = load_codes(v, i, FAST ? i + 4 : a.n, FAST || a.vec_s);
     };
-    load(i);
+    if constexpr (!AHEAD) load(i);
     for (int u = 0; u < blocks; ++u, i += kStateBlock) {
+      if constexpr (AHEAD) {
+        fetch(u + Ring<T>::STAGES - 1, i + (Ring<T>::STAGES - 1) * kStateBlock);
+        copy_async_wait<Ring<T>::STAGES - 1>();
+        const int at = u % Ring<T>::STAGES;
+        next.p = ring->p[at][threadIdx.x];
+        next.g = ring->g[at][threadIdx.x];
+        next.cm = ring->cm[at][threadIdx.x];
+        next.cv = ring->cv[at][threadIdx.x];
+      }
       Block4 x;
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
@@ -517,7 +562,8 @@ __device__ __forceinline__ bool run_chunk(const Table<CAP>& tab, int which, int6
       x.cv = next.cv;
       x.tm = __shfl_sync(0xffffffffu, old_me, u);
       x.tv = __shfl_sync(0xffffffffu, old_ve, u);
-      if (u + 1 < blocks) load(i + kStateBlock);
+      if constexpr (!AHEAD)
+        if (u + 1 < blocks) load(i + kStateBlock);
       Words4 w{};
       if (SR) w = stream_words(tab.keys, tag, s.t, (uint64_t)i >> 2);
       bad |= step_block<SR>(x, s, tab.c.b1, tab.c.b2, w);
@@ -542,6 +588,8 @@ __device__ __forceinline__ bool run_chunk(const Table<CAP>& tab, int which, int6
 template <typename T, int BITS, bool SR, int CAP>
 __global__ void __launch_bounds__(kThreads, BITS == 32 ? 5 : 3) adamw_kernel(const __grid_constant__ Table<CAP> tab) {
   __shared__ Step sh;
+  extern __shared__ __align__(16) uint8_t ring_bytes[];
+  Ring<T>* const ring = reinterpret_cast<Ring<T>*>(ring_bytes);   // BITS == 8
   tc::grid_dependency_wait();
   tc::grid_launch_dependents();
   if (threadIdx.x == 0) sh = make_step(tab.c);
@@ -560,9 +608,9 @@ __global__ void __launch_bounds__(kThreads, BITS == 32 ? 5 : 3) adamw_kernel(con
     const bool vec_p = (reinterpret_cast<uintptr_t>(t.p) & mask) == 0, vec_g = (reinterpret_cast<uintptr_t>(t.g) & mask) == 0;
     const bool vec_s = ((reinterpret_cast<uintptr_t>(t.m) | reinterpret_cast<uintptr_t>(t.v)) & state_mask) == 0;
     if (vec_p && vec_g && vec_s && base + (int64_t)tab.units * kUnit <= t.n)
-      bad |= run_chunk<T, BITS, SR>(tab, lo, base, View<T, true>{static_cast<T*>(t.p), static_cast<const T*>(t.g), t.m, t.v, t.n, true, true, true}, s);
+      bad |= run_chunk<T, BITS, SR>(tab, lo, base, View<T, true>{static_cast<T*>(t.p), static_cast<const T*>(t.g), t.m, t.v, t.n, true, true, true}, s, ring);
     else
-      bad |= run_chunk<T, BITS, SR>(tab, lo, base, View<T, false>{static_cast<T*>(t.p), static_cast<const T*>(t.g), t.m, t.v, t.n, vec_p, vec_g, vec_s}, s);
+      bad |= run_chunk<T, BITS, SR>(tab, lo, base, View<T, false>{static_cast<T*>(t.p), static_cast<const T*>(t.g), t.m, t.v, t.n, vec_p, vec_g, vec_s}, s, ring);
   }
   if (bad) raise_status(tab.status, METIS_DEV_NONFINITE);
 }
@@ -591,7 +639,7 @@ cudaError_t launch_cap(metis_ctx* ctx, const metis_adamw_tensor* const* ts, int 
   tab.count = count;
   tab.chunks = chunks;
   const int64_t grid = std::min<int64_t>(chunks, (int64_t)ctx->sm_count * (BITS == 32 ? 5 : 3));
-  return launch_early(adamw_kernel<T, BITS, SR, CAP>, grid, kThreads, 0, ctx->stream, tab);
+  return launch_early(adamw_kernel<T, BITS, SR, CAP>, grid, kThreads, kRing<T, BITS, SR> ? sizeof(Ring<T>) : 0, ctx->stream, tab);
 }
 
 template <typename T, int BITS, bool SR>

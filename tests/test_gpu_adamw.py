@@ -424,6 +424,28 @@ def test_more_than_two_to_the_31_elements(metis_lib):
     assert (opt.state[p]["exp_avg"][:first:1 << 20] == 0).all()
 
 
+@pytest.mark.parametrize("bits,rounding", [(8, "sr"), (8, "rn"), (32, "sr")])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_long_tensors_aligned_or_not_take_the_same_step(metis_lib, bits, rounding, dtype):
+    """Several state blocks a warp (whole chunks, and the ragged last one): arrays that start on 16 bytes
+    and arrays that start between take different loads to the same bits."""
+    from spectral_quantized_gemm_b200.optim import AdamW
+    n = 6_000_077
+    g = torch.Generator(device="cuda").manual_seed(5)
+    start = torch.randn(n, device="cuda", generator=g).to(dtype)
+    params = [torch.nn.Parameter(start.clone()), torch.nn.Parameter(torch.empty(n + 1, dtype=dtype, device="cuda")[1:].copy_(start))]
+    opts = [AdamW([p], state_bits=bits, rounding=rounding, **HYPER) for p in params]
+    for _ in range(3):
+        grad = (1e-2 * torch.randn(n, device="cuda", generator=g)).to(dtype)
+        for p, opt in zip(params, opts):
+            p.grad = grad if p is params[0] else torch.empty(n + 1, dtype=dtype, device="cuda")[1:].copy_(grad)
+            opt.step()
+    assert torch.equal(*[p.detach() for p in params])
+    for key in opts[0].state[params[0]]:
+        if key != "step":
+            assert torch.equal(*[opt.state[p][key] for p, opt in zip(params, opts)]), key
+
+
 def test_refusals(metis_lib):
     from spectral_quantized_gemm_b200.optim import AdamW
     p = torch.nn.Parameter(torch.zeros(300, device="cuda"))
