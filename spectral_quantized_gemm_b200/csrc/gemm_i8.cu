@@ -51,6 +51,19 @@ struct Params {
   uint32_t* status;
 };
 
+// A tile in S shares of K.  Tokens that a CTA finishes: a multiple of 4, so that four sums of a channel
+// travel as 16 bytes.  They lie as [share][four tokens][channel][token] in its shared memory: a warp's
+// store is 512 bytes in a row (with the channels apart it took twice as long).
+__host__ __device__ constexpr int own_tokens(int bn, int splits) { return (bn / splits + (bn % splits != 0) + 3) / 4 * 4; }
+constexpr int shared_sums(int bn) {   // bytes, for the S that needs most
+  int most = 0;
+  for (int s = 2; s <= kMaxSplits; ++s) {
+    const int b = s * own_tokens(bn, s) * 128 * 4;
+    most = b > most ? b : most;
+  }
+  return most;
+}
+
 template <int BN, bool SPLIT>
 struct Cfg {
   static constexpr int A_BYTES = BN * 128;             // tokens
@@ -59,12 +72,12 @@ struct Cfg {
   static constexpr int TMEM_COLS = BN < 32 ? 32 : BN;
   // Two or three CTAs fit an SM.  (Rings of 8 or 12 stages for a CTA that has its SM to itself were
   // no faster: 512 x 768 x 2304 7.1 us where 4 stages took 6.5.)
-  static constexpr int STAGES = SPLIT || BN == 32 ? 3 : 4;
-  static constexpr int PER_SM = BN == 16 || (BN == 32 && !SPLIT) ? 3 : 2;
+  static constexpr int STAGES = SPLIT && BN > 16 ? 5 : SPLIT || BN == 32 ? 3 : 4;
+  static constexpr int PER_SM = SPLIT && BN > 16 ? 1 : BN == 16 || (BN == 32 && !SPLIT) ? 3 : 2;
   static constexpr int PITCH = 128 + 4;                // words of a staged row of sums
-  // One CTA a tile: the sums take the ring's place.  Several: a place of their own, S times
-  // ceil(BN / S) rows, which may be written while this CTA still multiplies.
-  static constexpr int STAGED = (SPLIT ? BN + kMaxSplits - 1 : BN) * PITCH * 4;
+  // One CTA a tile: the sums take the ring's place.  Several: a place of their own, which may be written
+  // while this CTA still multiplies.
+  static constexpr int STAGED = SPLIT ? shared_sums(BN) : BN * PITCH * 4;
   static constexpr int RING = SPLIT || STAGES * STAGE_BYTES > STAGED ? STAGES * STAGE_BYTES : STAGED;
   static constexpr size_t SMEM = (size_t)RING + (SPLIT ? STAGED : 0) + (128 + BN) * 4 + 1024 + 256;
   static_assert(STAGED % 16 == 0 && (SMEM + 1024) * PER_SM <= 233472, "CTAs an SM");
@@ -95,7 +108,7 @@ __global__ void __launch_bounds__(kThreads)
 
   const int first = min(C::STAGES, s1 - s0);   // the first round of the ring
   // tokens of the tile, and this CTA's: own0 .. own1 - 1
-  const int rows = (int)min((int64_t)BN, p.p - (int64_t)cb * BN), share = (BN + splits - 1) / splits;
+  const int rows = (int)min((int64_t)BN, p.p - (int64_t)cb * BN), share = SPLIT ? own_tokens(BN, splits) : BN;
   const int own0 = min(rows, split * share), own1 = min(rows, own0 + share);
   if (threadIdx.x == 0) {
     for (int s = 0; s < C::STAGES; ++s) {
@@ -106,7 +119,7 @@ __global__ void __launch_bounds__(kThreads)
     if (SPLIT) tc::mbar_init(received, 1);
     *abort_flag = 0;
     tc::fence_barrier_init();
-    if (SPLIT) tc::mbar_expect_tx(received, (uint32_t)(splits * (own1 - own0) * 128 * 4));
+    if (SPLIT) tc::mbar_expect_tx(received, (uint32_t)(splits * ((own1 - own0 + 3) & ~3) * 128 * 4));
     // the first loads leave before the other threads are ready; in a chain B's under the tail of the
     // preceding kernel
     if (!p.early) tc::grid_dependency_wait();
@@ -122,7 +135,7 @@ __global__ void __launch_bounds__(kThreads)
   }
   tc::tc_fence_before();
   __syncthreads();
-  if (SPLIT) tc::cluster_arrive();   // this CTA's barrier is ready for the others' sums
+  if (SPLIT) tc::cluster_arrive_relaxed();   // this CTA's barrier is ready for the others' sums
   tc::tc_fence_after();
   const uint32_t tmem = *tmem_slot;
 
@@ -211,8 +224,8 @@ __global__ void __launch_bounds__(kThreads)
     const int quarter = warp & 3;
     const int row = quarter * 32 + lane;
     constexpr int W = BN < 32 ? 16 : 32;
-    // (SPLIT) where the sums of the current token go: CTA 0's first
-    const uint32_t here = tc::smem_addr(staged + split * share * C::PITCH + row);
+    // (SPLIT) where the sums of the current tokens go: CTA 0's first
+    const uint32_t here = tc::smem_addr(staged + split * share * 128 + row * 4);
     int owner = 0, left = share;
     uint32_t to = SPLIT ? tc::cluster_addr_u32(here, 0) : 0u, bar = SPLIT ? tc::cluster_addr_u32(tc::smem_addr(received), 0) : 0u;
 #pragma unroll
@@ -223,10 +236,11 @@ __global__ void __launch_bounds__(kThreads)
       tc::tmem_load_wait();
       if constexpr (SPLIT) {
 #pragma unroll
-        for (int i = 0; i < W; ++i) {
-          if (c + i < rows) tc::store_async(to, __float_as_uint(f[i]), bar);
-          to += C::PITCH * 4;
-          if (--left == 0) {                            // the next CTA's tokens
+        for (int i = 0; i < W; i += 4) {
+          if (c + i < rows)
+            tc::store_async4(to, __float_as_uint(f[i]), __float_as_uint(f[i + 1]), __float_as_uint(f[i + 2]), __float_as_uint(f[i + 3]), bar);
+          to += 128 * 16;
+          if ((left -= 4) == 0) {                       // the next CTA's tokens
             left = share;
             ++owner;
             to = tc::cluster_addr_u32(here, (uint32_t)min(owner, splits - 1));
@@ -245,28 +259,36 @@ __global__ void __launch_bounds__(kThreads)
     tc::tc_fence_after();
     tc::tmem_dealloc(tmem, C::TMEM_COLS);
   }
-  // This CTA's tokens: runs of 8 columns of C, a 16-byte store of bf16 or two of fp32.  Kept
-  // small (one output type, not unrolled): a CTA runs it once, and unrolled four times its
-  // instructions took 0.5 us longer to come in than they saved.
-  if (warp >= 2) {
-    // After a timeout too, the wait lasts until nothing more can arrive here.
-    const bool here = !SPLIT || own1 == own0 || tc::mbar_wait_cluster(received, 0);
+  const int cols = (int)min((int64_t)128, p.q - (int64_t)lb * 128);
+  OUT* const c0 = static_cast<OUT*>(p.C) + (int64_t)cb * BN * p.ldc + (int64_t)lb * 128;
+  if (SPLIT && warp >= 2) {
+    // This CTA's tokens, a thread a channel.  After a timeout too, the wait lasts until nothing more can
+    // arrive here.
+    const bool here = own1 == own0 || tc::mbar_wait_cluster(received, 0);
     if (!here && lane == 0) raise_status(p.status, METIS_DEV_TIMEOUT);
-    const int end = here ? own1 * (128 / 8) : 0;
+    const int t = (int)threadIdx.x - 64;
+    const float sj = sb[t];
+    for (int i = own0; here && t < cols && i < own1; i += 4) {
+      int4 a = make_int4(0, 0, 0, 0);
+      for (int s = 0; s < splits; ++s) {
+        const int4 x = *reinterpret_cast<const int4*>(staged + (s * share + i - own0) * 128 + t * 4);
+        a.x += x.x; a.y += x.y; a.z += x.z; a.w += x.w;
+      }
+      const int sums[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if (i + e < own1) c0[(int64_t)(i + e) * p.ldc + t] = (OUT)((float)sums[e] * sa[i + e] * sj);
+    }
+  } else if (!SPLIT && warp >= 2) {
+    // Runs of 8 columns of C, a 16-byte store of bf16 or two of fp32.  Kept small (one output type, not
+    // unrolled): a CTA runs it once, and unrolled four times its instructions took 0.5 us longer to
+    // come in than they saved.
     constexpr int RUNS = 128 / 8;
-    const int cols = (int)min((int64_t)128, p.q - (int64_t)lb * 128);
-    OUT* const c0 = static_cast<OUT*>(p.C) + (int64_t)cb * BN * p.ldc + (int64_t)lb * 128;
-    for (int u = own0 * RUNS + (int)threadIdx.x - 64; u < end; u += kThreads - 64) {
+    for (int u = (int)threadIdx.x - 64; u < rows * RUNS; u += kThreads - 64) {
       const int i = u / RUNS, j = (u % RUNS) * 8;
       if (j >= cols) continue;
-      const int* from = staged + (i - own0) * C::PITCH + j;
-      int4 a = *reinterpret_cast<const int4*>(from), b = *reinterpret_cast<const int4*>(from + 4);
-      for (int s = 1; s < splits; ++s) {
-        from += share * C::PITCH;
-        const int4 x = *reinterpret_cast<const int4*>(from), y = *reinterpret_cast<const int4*>(from + 4);
-        a.x += x.x; a.y += x.y; a.z += x.z; a.w += x.w;
-        b.x += y.x; b.y += y.y; b.z += y.z; b.w += y.w;
-      }
+      const int* from = staged + i * C::PITCH + j;
+      const int4 a = *reinterpret_cast<const int4*>(from), b = *reinterpret_cast<const int4*>(from + 4);
       const float si = sa[i];
       const float4 t0 = *reinterpret_cast<const float4*>(sb + j), t1 = *reinterpret_cast<const float4*>(sb + j + 4);
       const float o[8] = {(float)a.x * si * t0.x, (float)a.y * si * t0.y, (float)a.z * si * t0.z, (float)a.w * si * t0.w,

@@ -242,8 +242,9 @@ __device__ __forceinline__ uint32_t cluster_size() {
 __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
-// The two halves of that barrier, for work in between.
-__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+// The two halves of that barrier, for work in between.  Relaxed: what the others are to see is published by
+// fence_barrier_init (the releasing form waited 2 us for the loads under way).
+__device__ __forceinline__ void cluster_arrive_relaxed() { asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory"); }
 __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
 // shared::cluster address of the object at `p`'s offset in CTA `rank` of the cluster.
 __device__ __forceinline__ uint32_t cluster_addr(const void* p, uint32_t rank) {
@@ -261,10 +262,11 @@ __device__ __forceinline__ uint32_t cluster_addr_u32(uint32_t saddr, uint32_t ra
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar) {
   asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
-// Asynchronous store of a word to another CTA's shared memory of the cluster; its 4 bytes are counted
-// on the mbarrier `bar` of the same CTA (both shared::cluster addresses).
-__device__ __forceinline__ void store_async(uint32_t addr, uint32_t v, uint32_t bar) {
-  asm volatile("st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.u32 [%0], %1, [%2];" ::"r"(addr), "r"(v), "r"(bar)
+// Asynchronous store of four words to another CTA's shared memory of the cluster; its 16 bytes are
+// counted on the mbarrier `bar` of the same CTA (both shared::cluster addresses).
+__device__ __forceinline__ void store_async4(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d, uint32_t bar) {
+  asm volatile("st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.v4.u32 [%0], {%1, %2, %3, %4}, [%5];" ::"r"(addr),
+               "r"(a), "r"(b), "r"(c), "r"(d), "r"(bar)
                : "memory");
 }
 // mbar_wait for a phase that other CTAs of the cluster complete: acquires at cluster scope.
