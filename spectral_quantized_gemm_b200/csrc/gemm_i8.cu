@@ -70,7 +70,9 @@ struct Cfg {
   static constexpr int B_BYTES = 128 * 128;            // channels
   static constexpr int STAGE_BYTES = A_BYTES + B_BYTES;
   static constexpr int TMEM_COLS = BN < 32 ? 32 : BN;
-  // Two or three CTAs fit an SM.  (Rings of 8 or 12 stages for a CTA that has its SM to itself were
+  // Two or three CTAs fit an SM, but one of a share with more than 16 tokens, which has it to itself: 5
+  // stages (with quantizer: 40 x 4096 x 4096 9.45 us with 4, 9.55 with 5, 10.2 with 7; 60 x 14336 x 4096
+  // 17.8, 17.1, 17.8).  (Rings of 8 or 12 stages for a CTA that has its SM to itself were
   // no faster: 512 x 768 x 2304 7.1 us where 4 stages took 6.5.)
   static constexpr int STAGES = SPLIT && BN > 16 ? 5 : SPLIT || BN == 32 ? 3 : 4;
   static constexpr int PER_SM = SPLIT && BN > 16 ? 1 : BN == 16 || (BN == 32 && !SPLIT) ? 3 : 2;
