@@ -64,18 +64,22 @@ constexpr int shared_sums(int bn) {   // bytes, for the S that needs most
   return most;
 }
 
-template <int BN, bool SPLIT>
+// Many tiles, several CTAs an SM; up to one tile an SM; tiles in shares of K, each by a cluster (of two
+// CTAs at least: the stores between them need a cluster launch).
+enum Kind { kMany, kAlone, kShares };
+
+template <int BN, Kind KIND>
 struct Cfg {
+  static constexpr bool SPLIT = KIND == kShares;
   static constexpr int A_BYTES = BN * 128;             // tokens
   static constexpr int B_BYTES = 128 * 128;            // channels
   static constexpr int STAGE_BYTES = A_BYTES + B_BYTES;
   static constexpr int TMEM_COLS = BN < 32 ? 32 : BN;
-  // Two or three CTAs fit an SM, but one of a share with more than 16 tokens, which has it to itself: 5
-  // stages (with quantizer: 40 x 4096 x 4096 9.45 us with 4, 9.55 with 5, 10.2 with 7; 60 x 14336 x 4096
-  // 17.8, 17.1, 17.8).  (Rings of 8 or 12 stages for a CTA that has its SM to itself were
-  // no faster: 512 x 768 x 2304 7.1 us where 4 stages took 6.5.)
-  static constexpr int STAGES = SPLIT && BN > 16 ? 5 : SPLIT || BN == 32 ? 3 : 4;
-  static constexpr int PER_SM = SPLIT && BN > 16 ? 1 : BN == 16 || (BN == 32 && !SPLIT) ? 3 : 2;
+  // Stages of the ring.  A share with more than 16 tokens has its SM to itself: 5 (with quantizer: 40 x
+  // 4096 x 4096 9.45 us with 4, 9.55 with 5, 10.2 with 7; 60 x 14336 x 4096 17.8, 17.1, 17.8).  A single
+  // tile: 6 (32 x 4096 x 14336 18.2 us with 3, 15.7 with 6, 16.1 with 8).
+  static constexpr int STAGES = KIND == kAlone ? 6 : SPLIT && BN > 16 ? 5 : SPLIT || BN == 32 ? 3 : 4;
+  static constexpr int PER_SM = KIND == kAlone || (SPLIT && BN > 16) ? 1 : BN == 64 ? 2 : 3;
   static constexpr int PITCH = 128 + 4;                // words of a staged row of sums
   // One CTA a tile: the sums take the ring's place.  Several: a place of their own, which may be written
   // while this CTA still multiplies.
@@ -85,10 +89,11 @@ struct Cfg {
   static_assert(STAGED % 16 == 0 && (SMEM + 1024) * PER_SM <= 233472, "CTAs an SM");
 };
 
-template <int BN, bool SPLIT, typename OUT>
+template <int BN, Kind KIND, typename OUT>
 __global__ void __launch_bounds__(kThreads)
     gemm_i8_kernel(const __grid_constant__ CUtensorMap mapA, const __grid_constant__ CUtensorMap mapB, const Params p) {
-  using C = Cfg<BN, SPLIT>;
+  using C = Cfg<BN, KIND>;
+  constexpr bool SPLIT = C::SPLIT;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   float* sb = reinterpret_cast<float*>(smem + C::RING + (SPLIT ? C::STAGED : 0));   // scales of the tile's channels and tokens
@@ -577,9 +582,9 @@ bool make_map_i8(CUtensorMap* map, const metis_int8* t, uint32_t box_rows) {
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int BN, bool SPLIT, typename OUT>
+template <int BN, Kind KIND, typename OUT>
 metis_status launch_tile(metis_ctx* ctx, const metis_int8* A, const metis_int8* B, Params prm, int splits, bool chained) {
-  using C = Cfg<BN, SPLIT>;
+  using C = Cfg<BN, KIND>;
   CUtensorMap ma, mb;
   if (!make_map_i8(&ma, A, BN) || !make_map_i8(&mb, B, 128))
     return fail(ctx, METIS_ERR_CUDA, "cuTensorMapEncodeTiled failed for the int8 operands");
@@ -587,7 +592,7 @@ metis_status launch_tile(metis_ctx* ctx, const metis_int8* A, const metis_int8* 
   const int64_t ctas = lane_tiles * col_tiles * splits;
   if (ctas > INT32_MAX) return fail(ctx, METIS_ERR_SHAPE, "too many output tiles");
   prm.lane_tiles = (int)lane_tiles;
-  auto kern = gemm_i8_kernel<BN, SPLIT, OUT>;
+  auto kern = gemm_i8_kernel<BN, KIND, OUT>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::SMEM);
   if (e != cudaSuccess) return check_cuda(ctx, e, "cudaFuncSetAttribute(int8 gemm)");
   prm.early = chained;
@@ -640,22 +645,27 @@ metis_status launch_gemm_i8(metis_ctx* ctx, const metis_int8* A, const metis_int
   const int bn = prm.p <= 16 ? 16 : prm.p <= 32 ? 32 : 64;
   const int64_t tiles = ((prm.q + 127) / 128) * ((prm.p + bn - 1) / bn);
   // Tile kernel or CTA pairs.  While the tiles of the former fit the SMs at once (two each) it is
-  // ahead: 512 x 4096 x 4096 15.5 us against 18.5, 1024 x 1024 x 1024 6.1 against 9.2; with a
-  // second wave it is behind: 2048 x 512 x 2048 11.4 against 9.8.  Up to 128 rows of A leave half
+  // ahead: 512 x 4096 x 4096 15.3 us against 18.5, 1024 x 1024 x 1024 6.0 against 9.2; with a
+  // second wave it is behind: 2048 x 512 x 2048 11.2 against 9.9.  Up to 128 rows of A leave half
   // of a pair's tile empty.
   if (prm.p > 128 && tiles > 2 * ctx->sm_count) return launch_pair(ctx, A, B, prm);
-  // Shares of K.  Up to 16 tokens a join costs little, and more CTAs stream the weight faster
-  // (1 x 4096 x 4096: 11.9 us in one share, 6.8 in eight; 1 x 768 x 2304: 3.8, 3.3 in six;
-  // 1 x 4096 x 14336: 14.2, 12.6 in three, 16.6 in four, which no longer fit the SMs three to
-  // each).  With 32 or 64 the join moves more: one CTA an SM and eight blocks of K each (40 x 4096 x
-  // 4096: 13.1, 9.2 in four, 10.2 in eight; 512 x 2304 x 768: 8.8, 8.0 in two, 9.5 in three).
+  // Shares of K.  Up to 16 tokens several CTAs share an SM, and more of them stream the weight faster
+  // (1 x 4096 x 4096: 11.9 us in one share, 6.2 in eight; 1 x 768 x 2304: 3.8, 2.9 in six;
+  // 1 x 4096 x 14336: 14.0, 11.8 in three, 14.8 in four, which no longer fit the SMs three to
+  // each).  With 32 or 64 a CTA takes an SM to itself, and eight blocks of K each (40 x 4096 x
+  // 4096: 12.6, 7.8 in four, 12.2 in six; 60 x 14336 x 4096: 35.9, 15.1 in four, 21.4 in six; 512 x
+  // 2304 x 768: 8.6, 8.6 in two, 12.8 in three).
   const int64_t room = (bn == 16 ? ctx->sm_count * 27 / 10 : ctx->sm_count) / tiles;
   const int splits = (int)std::max<int64_t>(1, std::min<int64_t>({kMaxSplits, room, prm.k_tiles / (bn == 16 ? 1 : 8)}));
+  // The deeper ring where a weight is read once, from HBM, by up to one CTA an SM.  Where several CTAs read
+  // it from L2 it is no faster (256 x 4096 x 4096 15.1 us, 15.0 without; 512 x 768 x 2304 7.0, 6.7).
+  const bool alone = bn > 16 && prm.p <= bn && splits == 1 && tiles <= ctx->sm_count && prm.k_tiles >= 8;
   auto launch = [&](auto zero) {
     using OUT = decltype(zero);
-#define METIS_TILE(BN) \
-  (splits > 1 ? launch_tile<BN, true, OUT>(ctx, A, B, prm, splits, chained) : launch_tile<BN, false, OUT>(ctx, A, B, prm, 1, chained))
-    return bn == 16 ? METIS_TILE(16) : bn == 32 ? METIS_TILE(32) : METIS_TILE(64);
+#define METIS_TILE(BN, KIND) launch_tile<BN, KIND, OUT>(ctx, A, B, prm, splits, chained)
+    if (bn == 16) return splits > 1 ? METIS_TILE(16, kShares) : METIS_TILE(16, kMany);
+    if (bn == 32) return splits > 1 ? METIS_TILE(32, kShares) : alone ? METIS_TILE(32, kAlone) : METIS_TILE(32, kMany);
+    return splits > 1 ? METIS_TILE(64, kShares) : alone ? METIS_TILE(64, kAlone) : METIS_TILE(64, kMany);
 #undef METIS_TILE
   };
   return prm.f32 ? launch(float{}) : launch(__nv_bfloat16{});
