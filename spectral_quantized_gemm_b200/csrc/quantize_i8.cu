@@ -132,16 +132,26 @@ __device__ __forceinline__ Chunk<T> load_chunk(const T* row, int c, int cols, bo
   return k;
 }
 
+// The larger of `top` and |x|; NaN if one is (bf16: two numbers in a word).
+__device__ __forceinline__ uint32_t max_abs(uint32_t top, uint32_t x) {
+  asm("{\n\t.reg .f32 a;\n\tabs.f32 a, %1;\n\tmax.NaN.f32 %0, %2, a;\n\t}" : "=r"(top) : "r"(x), "r"(top));
+  return top;
+}
+__device__ __forceinline__ uint32_t max_abs2(uint32_t top, uint32_t x) {
+  asm("{\n\t.reg .b32 a;\n\tabs.bf16x2 a, %1;\n\tmax.NaN.bf16x2 %0, %2, a;\n\t}" : "=r"(top) : "r"(x), "r"(top));
+  return top;
+}
+
 // Largest |x| as fp32 bits (they order like the values); NaN and infinities give kInf or more.
 template <typename T>
 __device__ __forceinline__ uint32_t chunk_top(const Chunk<T>& k, uint32_t top) {
   if constexpr (sizeof(T) == 4) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) top = max(top, k.w[i] & 0x7FFFFFFFu);
+    for (int i = 0; i < 8; ++i) top = max_abs(top, k.w[i]);
   } else {
     uint32_t m = 0;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) m = __vmaxu2(m, k.w[i] & 0x7FFF7FFFu);
+    for (int i = 0; i < 4; ++i) m = max_abs2(m, k.w[i]);
     top = max(top, max(m << 16, m & 0xFFFF0000u));
   }
   return top;
@@ -208,8 +218,8 @@ constexpr int kCopies = METIS_INT8_SCRATCH_COPIES;
 // like the values).
 template <typename T>
 __device__ __forceinline__ uint32_t word_top(uint32_t top, uint32_t w) {
-  if constexpr (sizeof(T) == 2) return __vmaxu2(top, w & 0x7FFF7FFFu);
-  else return max(top, w & 0x7FFFFFFFu);
+  if constexpr (sizeof(T) == 2) return max_abs2(top, w);
+  else return max_abs(top, w);
 }
 template <int GROUP>
 __device__ __forceinline__ void group_sync(int group) {
