@@ -162,6 +162,18 @@ def test_product_is_exact(ctx, metis_lib, p, k, q, dtype):
     assert ctx.poll_device_status() == 0
 
 
+# K in 2 to 8 shares (a block of 128 each up to 16 tokens, eight above), tokens that do not divide by them, and single tiles
+SHARES = [(p, 128 * s - 5, q) for s in range(2, 9) for p, q in ((1, 130), (2 * s - 1, 40), (16, 257))] + \
+         [(p, 1024 * s + 77, q) for s in range(2, 9) for p, q in ((17 + s, 130), (33 + 3 * s, 72), (64, 129), (60 + 8 * s, 9))] + \
+         [(20, 1100, 10000), (63, 1030, 9601), (64, 1024, 18900)]
+
+
+@pytest.mark.parametrize("p,k,q", SHARES)
+def test_product_in_shares_is_exact(ctx, metis_lib, p, k, q):
+    test_product_is_exact(ctx, metis_lib, p, k, q, torch.float32)
+    test_product_is_exact(ctx, metis_lib, p, k, q, torch.bfloat16)
+
+
 @pytest.mark.parametrize("p,q", [(2, 3), (70, 130), (300, 260)])
 def test_product_at_the_ends_of_the_codes(ctx, metis_lib, p, q):
     """The largest sums there are: 131071 products of (-128) (-128), and of 127 (-128)."""
@@ -532,6 +544,27 @@ def test_frozen_layer_serves_and_notices_a_changed_weight(metis_lib):
     assert layer(x).requires_grad                          # training does not read the frozen codes
     with torch.no_grad():
         assert torch.equal(layer.freeze()(x), layer.unfreeze()(x))
+
+
+@pytest.mark.parametrize("rows", [1, 24, 60, 300])
+def test_served_right_after_the_weight_was_written(metis_lib, rows):
+    """A new weight, its layout, its use and the next weight in the same memory, with nothing in between that
+    waits: each answer belongs to its weight."""
+    layer = _layer(2048, 1536, 40)
+    x = _matrix(rows, 2048, torch.bfloat16, 41).cuda()
+    weights = [_matrix(2048, 1536, torch.float32, 50 + i).cuda() for i in range(4)]
+    want = []
+    with torch.no_grad():
+        for w in weights:
+            layer.weight.copy_(w)
+            want.append(layer(x))
+            torch.cuda.synchronize()
+        got = []
+        for i in range(24):
+            layer.weight.copy_(weights[i % 4])
+            got.append(layer.freeze()(x))
+        for i in range(24):
+            assert torch.equal(got[i], want[i % 4]), i
 
 
 def test_layer_on_another_stream(metis_lib):
