@@ -648,8 +648,9 @@ metis_status launch_gemm_i8(metis_ctx* ctx, const metis_int8* A, const metis_int
   // Tile kernel or CTA pairs.  While the tiles of the former fit the SMs at once (two each) it is
   // ahead: 512 x 4096 x 4096 15.3 us against 18.5, 1024 x 1024 x 1024 6.0 against 9.2; with a
   // second wave it is behind: 2048 x 512 x 2048 11.2 against 9.9.  Up to 128 rows of A leave half
-  // of a pair's tile empty.
-  if (prm.p > 128 && tiles > 2 * ctx->sm_count) return launch_pair(ctx, A, B, prm);
+  // of a pair's tile empty.  A pair's stores need a whole 16 bytes of columns (a tensor map's extent may
+  // not be 0), so a product by fewer stays with the tiles at any length.
+  if (prm.p > 128 && tiles > 2 * ctx->sm_count && whole_columns(prm.q, prm.f32) > 0) return launch_pair(ctx, A, B, prm);
   // Shares of K.  Up to 16 tokens several CTAs share an SM, and more of them stream the weight faster
   // (1 x 4096 x 4096: 11.9 us in one share, 6.2 in eight; 1 x 768 x 2304: 3.8, 2.9 in six;
   // 1 x 4096 x 14336: 14.0, 11.8 in three, 14.8 in four, which no longer fit the SMs three to

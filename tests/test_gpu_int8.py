@@ -577,3 +577,38 @@ def test_layer_on_another_stream(metis_lib):
         got = layer(x).detach()
     torch.cuda.current_stream().wait_stream(side)
     assert torch.equal(got, want)
+
+
+# the pair kernel's stores leave in 16 bytes: 8 bf16 or 4 fp32 columns
+NARROW = [(18945, 64, q) for q in (1, 3, 4, 5, 7, 8, 12)] + [(20000, 100, 3), (19000, 1000, 7), (40000, 16, 130)]
+
+
+@pytest.mark.parametrize("p,k,q", NARROW)
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_product_of_many_rows_by_few_columns(ctx, metis_lib, p, k, q, dtype):
+    test_product_is_exact(ctx, metis_lib, p, k, q, dtype)
+
+
+@pytest.mark.parametrize("q", [1, 3, 5, 7, 8, 40])
+def test_product_of_few_columns_on_few_sms(ctx, metis_lib, q):
+    ctx.set_sm_count_target(2)
+    try:
+        for dtype in (torch.bfloat16, torch.float32):
+            test_product_is_exact(ctx, metis_lib, 300, 200, q, dtype)
+    finally:
+        ctx.set_sm_count_target(0)
+
+
+@pytest.mark.parametrize("l,m,n", [(18945, 40, 1), (18945, 3, 24), (33, 18945, 3), (18950, 5, 6)])
+def test_layer_of_few_features_on_many_tokens(metis_lib, l, m, n):
+    layer = _layer(m, n, 1)
+    x = _matrix(l, m, torch.bfloat16, 2).cuda().requires_grad_(True)
+    dy = (1e-5 * _matrix(l, n, torch.float32, 3)).bfloat16().cuda()
+    y = layer(x)
+    y.backward(dy)
+    wy, wdx, wdw = _formula(_np(x), _np(layer.weight), _np(dy))
+    assert torch.equal(y.detach().cpu(), torch.from_numpy(wy).bfloat16())
+    assert torch.equal(x.grad.cpu(), torch.from_numpy(wdx).bfloat16())
+    assert torch.equal(layer.weight.grad.cpu(), torch.from_numpy(wdw))
+    with torch.no_grad():
+        assert torch.equal(layer.freeze()(x), y)
