@@ -37,9 +37,10 @@ MAX_INNER = 131071
 
 
 def _output(rows, cols, dtype, device):
-    """rows x cols with rows that start on 16 bytes."""
+    """rows x cols with rows that start on 16 bytes.  Not a view: autograd refuses in-place changes of a
+    view that a Function returns."""
     size = 8 if dtype == torch.bfloat16 else 4
-    return torch.empty(rows, -(-cols // size) * size, dtype=dtype, device=device)[:, :cols]
+    return torch.empty_strided((rows, cols), (-(-cols // size) * size, 1), dtype=dtype, device=device)
 
 
 def _operand(M):

@@ -612,3 +612,25 @@ def test_layer_of_few_features_on_many_tokens(metis_lib, l, m, n):
     assert torch.equal(layer.weight.grad.cpu(), torch.from_numpy(wdw))
     with torch.no_grad():
         assert torch.equal(layer.freeze()(x), y)
+
+
+@pytest.mark.parametrize("n", [48, 77])
+@pytest.mark.parametrize("shape", [(33,), (3, 11)])
+def test_layer_output_changed_in_place(metis_lib, n, shape):
+    layer, bias = _layer(64, n, 5), _matrix(1, n, torch.bfloat16, 6).cuda()[0].requires_grad_(True)
+    x = _matrix(33, 64, torch.bfloat16, 7).cuda().reshape(*shape, 64).requires_grad_(True)
+    keep = (torch.rand(*shape, n, device="cuda", generator=torch.Generator("cuda").manual_seed(0)) > 0.5).bfloat16()
+    got = {}
+    for inplace in (False, True):
+        y = layer(x)
+        if inplace:
+            y.mul_(keep)
+            y += bias
+            y.relu_()
+        else:
+            y = torch.relu(y * keep + bias)
+        got[inplace] = (y.detach(), *torch.autograd.grad(y.float().square().sum(), (x, layer.weight, bias)))
+    for a, b in zip(got[False], got[True]):
+        assert torch.equal(a, b)
+    y = torch.nn.functional.dropout(layer(x), 0.5, inplace=True)
+    assert ((y == 0) | (y == 2 * layer(x))).all() and y.any()

@@ -86,3 +86,11 @@ def test_entry_layout_matches_the_struct(metis_lib):
     T = metis_lib.AdamWTensor
     assert metis_lib.ctypes.sizeof(T) == 8 * optim.ENTRY_WORDS
     assert [getattr(T, f).offset for f, _ in T._fields_] == [0, 8, 16, 24, 32, 40, 48, 56, 60]
+
+
+@pytest.mark.parametrize("dtype,ld", [(torch.bfloat16, 80), (torch.float32, 80)])
+def test_layer_outputs_are_padded_and_no_views(metis_lib, dtype, ld):
+    from spectral_quantized_gemm_b200.int8_linear import _output
+    for rows, cols in ((3, 77), (1, 77), (3, ld), (0, 77)):
+        y = _output(rows, cols, dtype, "cpu")
+        assert y.shape == (rows, cols) and y.stride() == (ld, 1) and not y._is_view()
