@@ -15,7 +15,8 @@ the type of X and dW is fp32 (cast to the weight's type).  Between forward and b
 keeps the codes of X and W, not X itself.
 
 Serving: ``freeze()`` lays the 8-bit weight out once; calls without gradients then read it
-instead of quantizing the weight each time, until ``unfreeze()``.
+instead of quantizing the weight each time, until ``unfreeze()``.  They raise once the weight has changed,
+as far as torch counts its changes (``freeze`` says which it does not).
 
 To capture a training pass into a CUDA graph, run it once on the capturing stream first and let no
 graph of an earlier pass over the same leaves live on (torch's own rule: their gradients would be
@@ -149,19 +150,27 @@ class Int8Linear(torch.nn.Module):
 
     @torch.no_grad()
     def freeze(self):
-        """Lays out the 8-bit weight for serving; returns self."""
+        """Lays out the 8-bit weight for serving; returns self.
+
+        A weight that was written, replaced, cast or moved since makes the next served call raise.  Writes
+        that torch does not count are not seen -- through ``weight.data``, by a replayed graph: call freeze() again after those.  The weight's memory is held until unfreeze()."""
         lib, lock = _shared_context(self.weight.device)
         with lock:
             held = lib.new_int8(self.out_features, self.in_features)
             lib.quantize_int8(_operand(self.weight.detach()), colwise=held)
-        self._frozen = (held, self._weight_mark())
+        # with its memory held, no other tensor comes to lie at its address
+        self._frozen = (held, self.weight, self.weight.detach(), self._weight_version())
         return self
 
-    def _weight_mark(self):
-        """Differs once the weight was written, replaced, cast or moved through torch (a replayed graph
-        that writes it is not seen)."""
+    def _weight_version(self):
+        return self.weight._version
+
+    def _frozen_holds(self):
+        """Whether the weight is the one that was laid out, by its identity, place, type and version."""
+        _, weight, seen, version = self._frozen
         w = self.weight
-        return w._version, w.data_ptr(), w.dtype, w.device
+        return (w is weight and w.data_ptr() == seen.data_ptr() and w.dtype is seen.dtype and w.device == seen.device and
+                w.stride() == seen.stride() and self._weight_version() == version)
 
     def __getstate__(self):
         return dict(self.__dict__, _frozen=None)     # a copy lays its weight out itself
@@ -188,8 +197,8 @@ class Int8Linear(torch.nn.Module):
         return y if x.dim() == 2 else y.reshape(*x.shape[:-1], self.out_features)
 
     def _serve(self, x):
-        held, mark = self._frozen
-        if mark != self._weight_mark():
+        held = self._frozen[0]
+        if not self._frozen_holds():
             raise RuntimeError("the weight changed since freeze(); call freeze() or unfreeze()")
         rows = x.shape[0]
         if rows == 0:

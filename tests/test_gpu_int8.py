@@ -634,3 +634,48 @@ def test_layer_output_changed_in_place(metis_lib, n, shape):
         assert torch.equal(a, b)
     y = torch.nn.functional.dropout(layer(x), 0.5, inplace=True)
     assert ((y == 0) | (y == 2 * layer(x))).all() and y.any()
+
+
+def test_frozen_layer_notices_replaced_memory(metis_lib):
+    layer = _layer(256, 136, 42)
+    x = _matrix(8, 256, torch.bfloat16, 43).cuda()
+    other = _matrix(256, 136, torch.float32, 44)
+    with torch.no_grad():
+        layer.freeze()
+        for _ in range(2):
+            layer.weight.data = other.cuda()
+        with pytest.raises(RuntimeError):
+            layer(x)
+
+
+def test_frozen_layer_notices_a_round_trip_cast(metis_lib):
+    layer = _layer(256, 136, 42)
+    x = _matrix(8, 256, torch.bfloat16, 43).cuda()
+    with torch.no_grad():
+        layer.freeze()
+        layer.bfloat16().float()
+        with pytest.raises(RuntimeError):
+            layer(x)
+
+
+def test_frozen_layer_notices_another_parameter_on_its_memory(metis_lib):
+    layer = _layer(256, 136, 42)
+    x = _matrix(8, 256, torch.bfloat16, 43).cuda()
+    with torch.no_grad():
+        layer.weight = torch.nn.Parameter(layer.weight.data)
+        layer.freeze()
+        layer.weight.mul_(2)
+        layer.weight = torch.nn.Parameter(layer.weight.data)
+        with pytest.raises(RuntimeError):
+            layer(x)
+
+
+def test_frozen_layer_notices_a_transposed_weight(metis_lib):
+    layer = _layer(64, 64, 42)
+    x = _matrix(8, 64, torch.bfloat16, 43).cuda()
+    with torch.no_grad():
+        layer.freeze()
+        layer.weight.data = layer.weight.data.t()
+        with pytest.raises(RuntimeError):
+            layer(x)
+        assert torch.equal(layer.freeze()(x), layer.unfreeze()(x))
