@@ -153,7 +153,8 @@ class Int8Linear(torch.nn.Module):
         """Lays out the 8-bit weight for serving; returns self.
 
         A weight that was written, replaced, cast or moved since makes the next served call raise.  Writes
-        that torch does not count are not seen -- through ``weight.data``, by a replayed graph: call freeze() again after those.  The weight's memory is held until unfreeze()."""
+        that torch does not count are not seen -- through ``weight.data``, by a replayed graph, to a weight made
+        in inference mode: call freeze() again after those.  The weight's memory is held until unfreeze()."""
         lib, lock = _shared_context(self.weight.device)
         with lock:
             held = lib.new_int8(self.out_features, self.in_features)
@@ -163,7 +164,7 @@ class Int8Linear(torch.nn.Module):
         return self
 
     def _weight_version(self):
-        return self.weight._version
+        return None if self.weight.is_inference() else self.weight._version
 
     def _frozen_holds(self):
         """Whether the weight is the one that was laid out, by its identity, place, type and version."""

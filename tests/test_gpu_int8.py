@@ -679,3 +679,12 @@ def test_frozen_layer_notices_a_transposed_weight(metis_lib):
         with pytest.raises(RuntimeError):
             layer(x)
         assert torch.equal(layer.freeze()(x), layer.unfreeze()(x))
+
+
+def test_layer_made_and_served_in_inference_mode(metis_lib):
+    from spectral_quantized_gemm_b200.int8_linear import Int8Linear
+    x = _matrix(8, 256, torch.bfloat16, 43).cuda()
+    with torch.inference_mode():
+        layer = Int8Linear(256, 136, device="cuda")
+        want = layer(x)
+        assert torch.equal(layer.freeze()(x), want)
