@@ -282,6 +282,10 @@ __device__ __forceinline__ int block_top(int field) { return min(max(field - 102
 // their last place of the fp64 values; where a border between codes is that near (one element
 // in 10^5 of an fp32 gradient; a bf16 one meets borders exactly, one in 300) the fp64 route
 // decides.
+//   That takes a new exponent of the block at most kDrop octaves below the old.  The first moment's error
+// besides its two roundings (one unit together) is below 2^-43 |b1 m|, from the rest of beta1 and the sum
+// of the remainders, so below 2^(t_old - 42) in a block of exponent t_old; the unit of its smallest codes
+// is 2^(t_new - 37).  Six octaves make that two units; where terms cancel further the fp64 route decides.
 //   A magnitude is scaled so that the lowest normal octave of the codes is fp32's own: its bits
 // count the codes in steps of 2^20, gradual underflow included, and what is added to round up is
 // (field + 1/2) 2^-16 of a step, or to nearest half a step, less a unit unless the code is odd.
@@ -290,6 +294,7 @@ __device__ __forceinline__ uint32_t rounded(uint32_t bits, uint32_t field4) {   
   return SR ? bits + field4 + 8u : bits + 0x7FFFFu + ((bits >> 20) & 1u);
 }
 constexpr uint32_t kNear = 4;   // units
+constexpr int kDrop = 6;        // octaves
 
 // One state block of 128 elements in a warp, four to a lane.
 struct Block4 {
@@ -359,12 +364,12 @@ __device__ __forceinline__ bool step_block(Block4& x, const Step& s, double b1, 
 #pragma unroll
     for (int j = 0; j < 4; ++j) x.p[j] = stepped<true>(x.p[j], ym[j], yv[j], s);
   }
-  // the block's exponents (bits of positive floats order like them), open next to a power of two and
-  // beyond the range, where gradients that are not finite end up too
+  // the block's exponents (bits of positive floats order like them), open next to a power of two, where
+  // the first moments cancelled and beyond the range, where gradients that are not finite end up too
   const uint32_t top_m = __reduce_max_sync(0xffffffffu, __float_as_uint(hm)), top_v = __reduce_max_sync(0xffffffffu, hv);
   int tm = (int)(top_m >> 23) - 127, tv = (int)(top_v >> 23) - 127;
   const uint32_t edge = min((top_m + kNear) & 0x7FFFFFu, (top_v + kNear) & 0x7FFFFFu);
-  const bool open = !usual || tm > 14 || tm < -60 || tv > 30 || tv < -60 || edge <= 2 * kNear;
+  const bool open = !usual || tm > 14 || tm < max(-60, x.tm - kDrop) || tv > 30 || tv < -60 || edge <= 2 * kNear;
   bool odd = false;
   uint32_t om, ov, redo = 0;
   if (open) {

@@ -533,3 +533,36 @@ def test_layers_and_optimizer_together(metis_lib):
     with torch.no_grad():
         want = up(x)
         assert torch.equal(up.freeze()(x), want)
+
+
+def _cancelling(blocks, b1, seed):
+    """First moments of a block's top octave and gradients that cancel them to 2^-7 .. 2^-26 in one step (deeper from
+    block to block), a few whole cancellations among them."""
+    rng = np.random.default_rng(seed)
+    m = rng.integers(8, 16, (blocks, 128)) / 16.0 * rng.choice([-1.0, 1.0], (blocks, 128))
+    depth = np.linspace(5, 24, blocks)[:, None] + rng.uniform(0, 16, (blocks, 128)) * (rng.random((blocks, 128)) < 0.7)
+    g = -(b1 * m / (1 - b1)) * (1 + rng.choice([-1.0, 1.0], m.shape) * 2.0 ** -np.minimum(depth, 26))
+    return m.reshape(-1), g.astype(np.float32).reshape(-1)
+
+
+@pytest.mark.parametrize("rounding", ["rn", "sr"])
+@pytest.mark.parametrize("b1", [0.85, 0.9, 0.99])
+def test_first_moments_that_cancel(metis_lib, rounding, b1):
+    from spectral_quantized_gemm_b200.optim import AdamW
+    hyper = dict(HYPER, betas=(b1, 0.99))
+    starts = [(np.array([0.34375]), np.array([-1.947916865], np.float32))] + [_cancelling(60, b1, s) for s in range(4)]
+    m1, g1 = _cancelling(200, b1, 9)
+    starts += [(m1[i:i + 1], g1[i:i + 1]) for i in range(0, 128 * 200, 128)]           # blocks of one element
+    params = [torch.nn.Parameter(torch.ones(len(m), device="cuda")) for m, _ in starts]
+    opt = AdamW(params, state_bits=8, rounding=rounding, seed=3, **hyper)
+    refs = [Reference(p, i, 8, rounding, 3) for i, p in enumerate(params)]
+    for p, ref, (m, g) in zip(params, refs, starts):
+        ref.m, ref.v = adamw.encode(m, True), adamw.encode(m * m, False)
+        assert np.array_equal(adamw.decode(*ref.m, True), m)
+        opt.state[p] = {"step": 0, "exp_avg": torch.from_numpy(ref.m[0]).cuda(), "exp_avg_exponent": torch.from_numpy(ref.m[1]).cuda(),
+                        "exp_avg_sq": torch.from_numpy(ref.v[0]).cuda(), "exp_avg_sq_exponent": torch.from_numpy(ref.v[1]).cuda()}
+        p.grad = torch.from_numpy(g).cuda()
+    before = [_np(p) for p in params]
+    opt.step()
+    for p, ref, b, (m, g) in zip(params, refs, before, starts):
+        ref.step(b, g.astype(np.float64), p, opt.state[p], hyper, False)
