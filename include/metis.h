@@ -427,7 +427,8 @@ metis_status metis_int8_linear_bwd(metis_ctx* ctx, const metis_dense* D, metis_i
  * Values beyond the largest code (within the block's top octave) take it; a positive v
  * takes code 1 at least.  All zero bytes are a fresh state.  8-bit moments are computed in
  * fp64, in the order b1 m + (1 - b1) g and b2 v + (1 - b2) (g g), each operation rounded;
- * the parameter (fp32 arithmetic) is updated with them before they become codes.
+ * the parameter (fp32 arithmetic, in which a v beyond 2^128 is infinite and its step zero) is
+ * updated with them before they become codes.
  * rounding 0: codes and bf16 parameters to nearest, ties to even; 1: stochastic, with
  * Philox words of key seed and counter (e / 4 lo, hi, id << 8 | 4 << 4 | sub, t) for
  * element e of the tensor, word e % 4: a code is floor(x + (r + 1/2) 2^-16) in units of its

@@ -333,7 +333,8 @@ __device__ __forceinline__ bool step_block(Block4& x, const Step& s, double b1, 
     const Pair add = Pair(s.a1) * g;
     const Pair rest = fma2(b1m_low, om, fma2(Pair(-s.a1_low), g, fma2(Pair(-s.a1), g, add)));
     fma2(rest, Pair(-1.0f), fma2(b1m, om, add)).get(ym[j], ym[j + 1]);
-    fma2(b2v, ov, Pair(s.a2) * (g * g)).get(yv[j], yv[j + 1]);   // five roundings: three units
+    // five roundings: three units; (1 - b2) g first, since g g leaves fp32 from 1.8e19 on
+    fma2(b2v, ov, Pair(s.a2) * g * g).get(yv[j], yv[j + 1]);
   }
   if (!usual) {
 #pragma unroll
@@ -496,7 +497,7 @@ __device__ __forceinline__ bool run_chunk(const Table<CAP>& tab, int which, int6
         const float g = fg.get(j), old = fm.get(j);
         z = fmaf(g, 0.0f, z);
         xm[j] = fmaf(s.b1, old, fmaf(s.b1_low, old, s.a1 * g));
-        xv[j] = fmaf(s.b2, fv.get(j), s.a2 * (g * g));
+        xv[j] = fmaf(s.b2, fv.get(j), s.a2 * g * g);   // in this order: g g alone leaves fp32 from 1.8e19 on
         xp[j] = s.tiny ? stepped<true>(fp.get(j), xm[j], xv[j], s) : stepped<false>(fp.get(j), xm[j], xv[j], s);
       }
       bad |= z != z;

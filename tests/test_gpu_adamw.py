@@ -566,3 +566,17 @@ def test_first_moments_that_cancel(metis_lib, rounding, b1):
     opt.step()
     for p, ref, b, (m, g) in zip(params, refs, before, starts):
         ref.step(b, g.astype(np.float64), p, opt.state[p], hyper, False)
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_gradients_whose_square_leaves_fp32(metis_lib, bits, dtype):
+    """g^2 is beyond fp32 from 1.8e19 on, (1 - b2) g^2 is not."""
+    from spectral_quantized_gemm_b200.optim import AdamW
+    hyper = dict(HYPER, betas=(0.9, 0.999))
+    params = _params([(700,)], dtype, 5)
+    opt = AdamW(params, state_bits=bits, rounding="rn", **hyper)
+    refs = [Reference(params[0], 0, bits, "rn", 0)]
+    g = torch.cat([torch.tensor([0.0, 2e19, -2e19, 1e20, -1e20, 1e18, 3e17, 1.0]), torch.zeros(300), torch.full((392,), 4e19)])
+    _run(opt, params, refs, 3, hyper, lambda p, s: (g if s < 2000 else -0.5 * g).to(dtype).cuda())
+    assert torch.isfinite(params[0]).all() and all(torch.isfinite(s.float()).all() for s in opt.state[params[0]].values() if isinstance(s, torch.Tensor))
