@@ -427,7 +427,8 @@ __global__ void __launch_bounds__(kThreads, 4) quantize_i8_cols_kernel(const T* 
     if (c0 + j < cols)
 #pragma unroll 8
       for (int r = threadIdx.x / COLS; r < n; r += kThreads / COLS, src += (kThreads / COLS) * ld)
-        *(reinterpret_cast<T*>(data + (r / kPiece) * kPieceBytes + (r % kPiece) * kRowBytes) + j) = *src;
+        // from L2, as cp.async.cg: read before the wait, when this SM's cache may hold an older matrix
+        *(reinterpret_cast<T*>(data + (r / kPiece) * kPieceBytes + (r % kPiece) * kRowBytes) + j) = __ldcg(src);
   }
   tc::grid_dependency_wait();   // for the maxima
   tc::grid_launch_dependents();

@@ -688,3 +688,26 @@ def test_layer_made_and_served_in_inference_mode(metis_lib):
         layer = Int8Linear(256, 136, device="cuda")
         want = layer(x)
         assert torch.equal(layer.freeze()(x), want)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("p,q", [(513, 333), (1500, 1031)])
+def test_columns_right_after_the_matrix_was_written(ctx, metis_lib, p, q, dtype):
+    """A product writes a matrix whose rows are quantized from an odd column on, and the next one writes the same
+    memory, with nothing in between that waits: each result belongs to its product."""
+    k, n = 256, 4
+    B = metis_lib.Int8(q, k, codes=_codes(q, k, 1)[0], scales=torch.ones(q, device="cuda"))
+    As = [metis_lib.Int8(p, k, codes=_codes(p, k, 2 + i)[0], scales=torch.full((p,), 2.0 ** -i, device="cuda")) for i in range(n)]
+    C = torch.empty(p, -(-q // 8) * 8, dtype=dtype, device="cuda")
+    M = C[:, 1:q]
+    want = []
+    for A in As:
+        ctx.gemm_int8(A, B, C[:, :q])
+        torch.cuda.synchronize()
+        want.append(tuple(torch.from_numpy(x).cuda() for x in int8.quantize_rows(_np(M).T)))
+    got = [ctx.new_int8(q - 1, p).with_scratch() for _ in range(6 * n)]
+    for i, col in enumerate(got):
+        ctx.gemm_int8(As[i % n], B, C[:, :q])
+        ctx.quantize_int8(M, colwise=col)
+    for i, col in enumerate(got):
+        assert torch.equal(col.codes, want[i % n][0]) and torch.equal(col.scales, want[i % n][1]), i
