@@ -15,7 +15,8 @@ lost on average by the nearest rounding and kept by the stochastic one.
 
 ``state_bits``, ``rounding``, ``lr``, ``betas``, ``eps`` and ``weight_decay`` may be set for each
 parameter group.  With ``capturable=True`` the step count of a group lives on the device
-(one for all its parameters) and ``lr`` may be a one-element fp32 CUDA tensor, so that step() can be
+(one for all its parameters; it goes on from theirs, and theirs from it, where a group's
+``capturable`` is changed between steps) and ``lr`` may be a one-element fp32 CUDA tensor, so that step() can be
 captured into a CUDA graph and replayed; take one step before the capture, which creates
 the states.  There is no CPU path.
 """
@@ -185,6 +186,8 @@ class AdamW(torch.optim.Optimizer):
         """The step from a plan that still holds; False if it does not."""
         if torch.cuda.is_current_stream_capturing() and not group["capturable"]:
             return False
+        if group["capturable"] != (group.get("step_count") is not None):     # changed since: the counts move first
+            return False
         t = None if group["capturable"] else plan.states[0]["step"]
         if not plan.renew(group["params"], self.state, _KEYS[group["state_bits"]], t):
             return False
@@ -221,6 +224,10 @@ class AdamW(torch.optim.Optimizer):
         state_dtype = torch.uint8 if bits == 8 else torch.float32
         states = self.state
         t = None
+        if not capturable and (count := group.pop("step_count", None)) is not None:
+            for p in group["params"]:                            # the group was capturable until now
+                if p in states:
+                    states[p]["step"] = int(count)
         for i, p, g in todo:
             dtype, n = p.dtype, p.numel()
             if not (g.layout is torch.strided and g.dtype is dtype and g.numel() == n and p.device == g.device and p.is_cuda):
@@ -264,7 +271,10 @@ class AdamW(torch.optim.Optimizer):
             if count is None:
                 if capturing:
                     raise RuntimeError("take one step before the capture: it creates the states")
-                count = group["step_count"] = torch.zeros((), dtype=torch.int64, device=device)
+                steps = {int(states[p]["step"]) for p in group["params"] if p in states} - {0}
+                if len(steps) > 1:
+                    raise ValueError("the parameters of a capturable group must have taken the same number of steps")
+                count = group["step_count"] = torch.full((), max(steps, default=0), dtype=torch.int64, device=device)
             count += 1
         for state, step in counted:
             state["step"] = step

@@ -580,3 +580,29 @@ def test_gradients_whose_square_leaves_fp32(metis_lib, bits, dtype):
     g = torch.cat([torch.tensor([0.0, 2e19, -2e19, 1e20, -1e20, 1e18, 3e17, 1.0]), torch.zeros(300), torch.full((392,), 4e19)])
     _run(opt, params, refs, 3, hyper, lambda p, s: (g if s < 2000 else -0.5 * g).to(dtype).cuda())
     assert torch.isfinite(params[0]).all() and all(torch.isfinite(s.float()).all() for s in opt.state[params[0]].values() if isinstance(s, torch.Tensor))
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+def test_counts_follow_a_change_of_capturable(metis_lib, bits):
+    from spectral_quantized_gemm_b200.optim import AdamW
+    runs = []
+    for change in (False, True):
+        params = _params([(500,), (30, 40)], torch.float32, 14)
+        opt = AdamW(params, state_bits=bits, seed=8, **HYPER)
+        for s in range(9):
+            if change and s in (3, 6):
+                opt.param_groups[0]["capturable"] = s == 3
+            for i, p in enumerate(params):
+                p.grad = _gradient(p, 10 * s + i)
+            opt.step()
+        runs.append((params, opt))
+    (a, opt_a), (b, opt_b) = runs
+    for p, q in zip(a, b):
+        assert torch.equal(p, q) and opt_b.state[q]["step"] == opt_a.state[p]["step"] == 9
+        assert torch.equal(opt_a.state[p]["exp_avg_sq"], opt_b.state[q]["exp_avg_sq"])
+    b[0].grad, b[1].grad = _gradient(b[0], 1), None
+    opt_b.step()
+    opt_b.param_groups[0]["capturable"] = True             # ten steps and nine: no count for both
+    b[1].grad = _gradient(b[1], 2)
+    with pytest.raises(ValueError):
+        opt_b.step()
