@@ -223,7 +223,7 @@ class AdamW(torch.optim.Optimizer):
         counted = []    # (state, its next step), set once all is checked
         state_dtype = torch.uint8 if bits == 8 else torch.float32
         states = self.state
-        t = None
+        t, fresh = None, 0
         if not capturable and (count := group.pop("step_count", None)) is not None:
             for p in group["params"]:                            # the group was capturable until now
                 if p in states:
@@ -240,6 +240,7 @@ class AdamW(torch.optim.Optimizer):
                 if capturing:
                     raise RuntimeError("take one step before the capture: it creates the states")
                 state.update(self._new_state(p, bits))
+                fresh += 1
             m, v = state["exp_avg"], state["exp_avg_sq"]
             if not (m.dtype is state_dtype and v.dtype is state_dtype and m.numel() == n and v.numel() == n and
                     m.device == v.device == p.device and
@@ -271,10 +272,12 @@ class AdamW(torch.optim.Optimizer):
             if count is None:
                 if capturing:
                     raise RuntimeError("take one step before the capture: it creates the states")
-                steps = {int(states[p]["step"]) for p in group["params"] if p in states} - {0}
+                steps = {int(states[p].get("step", 0)) for p in group["params"] if p in states} - {0}
                 if len(steps) > 1:
                     raise ValueError("the parameters of a capturable group must have taken the same number of steps")
                 count = group["step_count"] = torch.full((), max(steps, default=0), dtype=torch.int64, device=device)
+            elif fresh and fresh == sum("exp_avg" in states[p] for p in group["params"] if p in states):
+                count.zero_()                                    # no state has seen a step of it
             count += 1
         for state, step in counted:
             state["step"] = step

@@ -606,3 +606,17 @@ def test_counts_follow_a_change_of_capturable(metis_lib, bits):
     b[1].grad = _gradient(b[1], 2)
     with pytest.raises(ValueError):
         opt_b.step()
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+def test_replaced_states_restart_the_count_on_the_device(metis_lib, bits):
+    from spectral_quantized_gemm_b200.optim import AdamW
+    params, plain = _params([(500,)], torch.float32, 15), _params([(500,)], torch.float32, 15)
+    opts = [AdamW(params, state_bits=bits, seed=8, capturable=True, **HYPER), AdamW(plain, state_bits=bits, seed=8, **HYPER)]
+    for s in range(6):
+        for p, opt in zip((params[0], plain[0]), opts):
+            if s == 3:
+                opt.state.clear()
+            p.grad = _gradient(p, s)
+            opt.step()
+    assert torch.equal(params[0], plain[0]) and opts[0].param_groups[0]["step_count"].item() == 3
