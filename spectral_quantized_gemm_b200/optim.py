@@ -69,7 +69,7 @@ class _Plan:
         return list(map(_address, self.tensors))
 
     def renew(self, params, all_states, keys, t):
-        """Whether the plan holds; then its entries are those of the step t (None: not counted here)."""
+        """Whether the plan holds for states of t steps (None: not counted there); then its entries are up to date."""
         if len(params) != len(self.params) or not all(map(operator.is_, params, self.params)) or \
                 len(all_states) != len(self.all_states) or not all(map(operator.is_, all_states.values(), self.all_states)):
             return False
@@ -83,8 +83,6 @@ class _Plan:
         if t is not None:
             if list(map(_step, self.states)).count(t) != len(params):
                 return False
-            for s in self.states:
-                s["step"] = t + 1
         self.entries[1::ENTRY_WORDS] = array.array("Q", map(_address, grads))
         return True
 
@@ -191,21 +189,31 @@ class AdamW(torch.optim.Optimizer):
         t = None if group["capturable"] else plan.states[0]["step"]
         if not plan.renew(group["params"], self.state, _KEYS[group["state_bits"]], t):
             return False
-        if t is None:
-            group["step_count"] += 1
         self._launch(group, plan.device, t, plan.entries)
+        if t is not None:
+            for state in plan.states:
+                state["step"] = t + 1
         _increment_version(plan.params)
         return True
 
     def _launch(self, group, device, t, rows):
+        """One call for the entries of a device; t: their steps so far, or None for the group's count."""
         lr, (b1, b2) = group["lr"], group["betas"]
         on_device = isinstance(lr, torch.Tensor)
         lib, lock = _shared_context(device)
-        with lock:
-            lib.adamw_step(rows.buffer_info()[0], len(rows) // ENTRY_WORDS, 0.0 if on_device else float(lr), b1, b2,
-                           group["eps"], group["weight_decay"], 1 if t is None else t + 1, group["state_bits"],
-                           1 if group["rounding"] == "sr" else 0, self.seed, lr_dev=lr if on_device else None,
-                           step_dev=group["step_count"] if t is None else None)
+        count = group["step_count"] if t is None else None
+        if count is not None:
+            count += 1
+        try:
+            with lock:
+                lib.adamw_step(rows.buffer_info()[0], len(rows) // ENTRY_WORDS, 0.0 if on_device else float(lr), b1, b2,
+                               group["eps"], group["weight_decay"], 1 if t is None else t + 1, group["state_bits"],
+                               1 if group["rounding"] == "sr" else 0, self.seed, lr_dev=lr if on_device else None,
+                               step_dev=count)
+        except Exception:
+            if count is not None:
+                count -= 1                                       # a step that was refused does not count
+            raise
 
     def _step_group(self, group, first):
         bits, capturable = group["state_bits"], group["capturable"]
@@ -220,7 +228,7 @@ class AdamW(torch.optim.Optimizer):
             raise RuntimeError("step() under capture needs capturable=True")
         calls = {}      # (device, steps taken) -> flat list of the entries' numbers
         keep = []       # gradients copied into their parameter's layout
-        counted = []    # (state, its next step), set once all is checked
+        counted = []    # (state, its next step), set once all is launched
         state_dtype = torch.uint8 if bits == 8 else torch.float32
         states = self.state
         t, fresh = None, 0
@@ -278,11 +286,10 @@ class AdamW(torch.optim.Optimizer):
                 count = group["step_count"] = torch.full((), max(steps, default=0), dtype=torch.int64, device=device)
             elif fresh and fresh == sum("exp_avg" in states[p] for p in group["params"] if p in states):
                 count.zero_()                                    # no state has seen a step of it
-            count += 1
-        for state, step in counted:
-            state["step"] = step
         for (device, t), rows in calls.items():
             self._launch(group, device, t, rows)
+        for state, step in counted:
+            state["step"] = step
         _increment_version([p for _, p, _ in todo])
         # a plan for the next step where this one was regular
         if len(calls) > 1 or keep or len(todo) != len(group["params"]) or not all(p.is_contiguous() for _, p, _ in todo):

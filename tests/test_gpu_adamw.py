@@ -620,3 +620,27 @@ def test_replaced_states_restart_the_count_on_the_device(metis_lib, bits):
             p.grad = _gradient(p, s)
             opt.step()
     assert torch.equal(params[0], plain[0]) and opts[0].param_groups[0]["step_count"].item() == 3
+
+
+@pytest.mark.parametrize("capturable", [False, True])
+def test_a_refused_step_is_not_counted(metis_lib, capturable):
+    from spectral_quantized_gemm_b200.optim import AdamW
+    p = torch.nn.Parameter(torch.ones(300, device="cuda"))
+    opt = AdamW([p], capturable=capturable, **HYPER)
+
+    def count():
+        return opt.param_groups[0]["step_count"].item() if capturable else opt.state[p]["step"]
+
+    for steps in (1, 2):                                   # a plan is there from the second on
+        p.grad = torch.ones_like(p)
+        opt.step()
+        for fresh in (False, True):
+            opt.param_groups[0]["eps"] = -1.0
+            p.grad = torch.ones_like(p)
+            if fresh:
+                opt._plans.clear()
+            before = p.detach().clone()
+            with pytest.raises(metis_lib.MetisError):
+                opt.step()
+            opt.param_groups[0]["eps"] = 1e-8
+            assert count() == steps and torch.equal(p, before)
