@@ -93,6 +93,7 @@ __device__ Step make_step(const Coef& c) {
   s.size = (float)(lr / one_minus_power(c.b1, t));
   s.rbc2 = (float)(1.0 / sqrt(one_minus_power(c.b2, t)));
   s.eps = (float)c.eps;
+  if (s.eps == 0.0f && c.eps > 0.0) s.eps = __uint_as_float(1u);   // the smallest fp32: m = v = 0 stays 0 / eps
   s.b1 = __uint_as_float(__float_as_uint((float)c.b1) & ~15u);
   s.b1_low = (float)(c.b1 - (double)s.b1);
   s.a1 = (float)(1.0 - c.b1);

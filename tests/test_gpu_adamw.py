@@ -644,3 +644,17 @@ def test_a_refused_step_is_not_counted(metis_lib, capturable):
                 opt.step()
             opt.param_groups[0]["eps"] = 1e-8
             assert count() == steps and torch.equal(p, before)
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+def test_smallest_eps(metis_lib, bits):
+    """An eps below fp32's smallest number still keeps 0 / (0 + eps) at 0."""
+    from spectral_quantized_gemm_b200.optim import AdamW
+    for eps in (1e-50, 1e-45, 1e-40, 1e-300):
+        p = torch.nn.Parameter(torch.ones(300, device="cuda"))
+        opt = AdamW([p], lr=1e-2, eps=eps, weight_decay=0.0, state_bits=bits, rounding="rn")
+        p.grad = torch.zeros_like(p)
+        p.grad[::3] = 1e-3
+        opt.step()
+        opt.step()
+        assert (p[1::3] == 1).all() and torch.isfinite(p).all() and (p[::3] < 1).all()
