@@ -22,8 +22,8 @@ To capture a training pass into a CUDA graph, run it once on the capturing strea
 graph of an earlier pass over the same leaves live on (torch's own rule: their gradients would be
 gathered on that pass's stream).
 
-Any number of tokens and features is allowed (in_features, and out_features and tokens of
-a backward pass, up to 131071, the bound of the exact sum).  There is no CPU path.
+in_features and out_features go up to 131071, the bound of the exact sum, and so do the tokens
+of a pass that the weight gets a gradient from; other passes take any number.  There is no CPU path.
 """
 
 import functools
@@ -188,8 +188,8 @@ class Int8Linear(torch.nn.Module):
             raise ValueError(f"x is on {x.device}, the weight on {weight.device}")
         flat = x if x.dim() == 2 else x.reshape(-1, self.in_features)
         if torch.is_grad_enabled() and (x.requires_grad or weight.requires_grad):
-            if flat.shape[0] > MAX_INNER:
-                raise ValueError(f"at most {MAX_INNER} tokens in a pass with gradients, got {flat.shape[0]}")
+            if weight.requires_grad and flat.shape[0] > MAX_INNER:     # dW contracts the tokens
+                raise ValueError(f"at most {MAX_INNER} tokens in a pass with a gradient of the weight, got {flat.shape[0]}")
             y = _Int8LinearFn.apply(flat, weight)
         elif self._frozen is not None:
             y = self._serve(flat)

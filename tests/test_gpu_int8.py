@@ -711,3 +711,14 @@ def test_columns_right_after_the_matrix_was_written(ctx, metis_lib, p, q, dtype)
         ctx.quantize_int8(M, colwise=col)
     for i, col in enumerate(got):
         assert torch.equal(col.codes, want[i % n][0]) and torch.equal(col.scales, want[i % n][1]), i
+
+
+def test_frozen_weight_takes_any_number_of_tokens(metis_lib):
+    layer = _layer(16, 24, 50)
+    layer.weight.requires_grad_(False)
+    x = _matrix(131072 + 5, 16, torch.bfloat16, 51).cuda().requires_grad_(True)
+    y = layer(x)
+    y.sum().backward()
+    wy, wdx, _ = _formula(_np(x), _np(layer.weight), np.ones((131072 + 5, 24)))
+    assert torch.equal(y.detach().cpu(), torch.from_numpy(wy).bfloat16())
+    assert torch.equal(x.grad.cpu(), torch.from_numpy(wdx).bfloat16())
