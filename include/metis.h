@@ -381,7 +381,7 @@ metis_status metis_gemm_int8(metis_ctx* ctx, const metis_int8* A, const metis_in
 /*
  * Linear layer on held 8-bit weights: quantizes X (p x K, as metis_quantize_int8 row-wise)
  * into Xq (p x K, caller-owned, written) and computes C = Xq W^T as metis_gemm_int8 with
- * W (q x K, a scale for each output channel).
+ * W (q x K, a scale for each output channel).  Xq and W must not overlap.
  */
 metis_status metis_linear_int8(metis_ctx* ctx, const void* X, int64_t ld, int32_t dtype, metis_int8* Xq,
                                const metis_int8* W, void* C, int64_t ldc, int32_t c_dtype);

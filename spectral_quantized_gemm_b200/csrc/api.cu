@@ -723,6 +723,9 @@ metis_status metis_linear_int8(metis_ctx* ctx, const void* X, int64_t ld, int32_
     if (!Xq) return fail(ctx, METIS_ERR_ARG, "null operand");
     metis_status s = check_quantize_int8(ctx, X, Xq->outer, Xq->inner, ld, dtype, Xq, nullptr);
     if (s != METIS_OK || (s = check_gemm_int8(ctx, Xq, W, C, ldc, c_dtype)) != METIS_OK) return s;
+    // the product reads W while the quantizer still writes Xq
+    if (Xq->codes == W->codes || Xq->scales == W->scales)
+      return fail(ctx, METIS_ERR_ARG, "Xq and W need codes and scales of their own");
     const metis_dense dense{X, Xq->outer, Xq->inner, ld, dtype};
     s = quantize_int8(ctx, &dense, Xq, nullptr);
     return s == METIS_OK ? launch_gemm_i8(ctx, Xq, W, C, ldc, c_dtype, true) : s;

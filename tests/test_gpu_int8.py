@@ -722,3 +722,15 @@ def test_frozen_weight_takes_any_number_of_tokens(metis_lib):
     wy, wdx, _ = _formula(_np(x), _np(layer.weight), np.ones((131072 + 5, 24)))
     assert torch.equal(y.detach().cpu(), torch.from_numpy(wy).bfloat16())
     assert torch.equal(x.grad.cpu(), torch.from_numpy(wdx).bfloat16())
+
+
+def test_linear_refuses_its_weight_as_the_buffer(ctx, metis_lib):
+    W = ctx.new_int8(8, 32)
+    X, Y = torch.zeros(8, 32, device="cuda"), torch.zeros(8, 8, device="cuda")
+    with pytest.raises(metis_lib.MetisError) as e:
+        ctx.linear_int8(X, W, W, Y)
+    assert e.value.status == 1
+    for kw in (dict(scales=W.scales), dict(codes=W.codes)):
+        with pytest.raises(metis_lib.MetisError) as e:
+            ctx.linear_int8(X, metis_lib.Int8(8, 32, **kw), W, Y)
+        assert e.value.status == 1
