@@ -144,8 +144,9 @@ class AdamW(torch.optim.Optimizer):
                 else:
                     self.state[p][name] = value
         for group in self.param_groups:
-            if isinstance(group.get("step_count"), torch.Tensor) and group["params"]:
-                group["step_count"] = group["step_count"].to(device=group["params"][0].device, copy=True)
+            for name in ("step_count", "lr"):
+                if isinstance(group.get(name), torch.Tensor) and group["params"]:
+                    group[name] = group[name].to(device=group["params"][0].device, copy=True)
 
     # -- the step ----------------------------------------------------------------------
     def _new_state(self, p, bits):

@@ -658,3 +658,32 @@ def test_smallest_eps(metis_lib, bits):
         opt.step()
         opt.step()
         assert (p[1::3] == 1).all() and torch.isfinite(p).all() and (p[::3] < 1).all()
+
+
+def test_checkpoint_of_a_learning_rate_on_the_device(metis_lib):
+    import io
+    from spectral_quantized_gemm_b200.optim import AdamW
+    hyper = {k: v for k, v in HYPER.items() if k != "lr"}
+
+    def make():
+        params = _params([(300,)], torch.float32, 16)
+        return params[0], AdamW(params, lr=torch.tensor(1e-2, device="cuda"), state_bits=8, capturable=True, **hyper)
+
+    def train(p, opt, first):
+        for s in range(first, first + 2):
+            opt.param_groups[0]["lr"].mul_(0.5)
+            p.grad = _gradient(p, s)
+            opt.step()
+
+    p, opt = make()
+    train(p, opt, 0)
+    buf, start = io.BytesIO(), p.detach().clone()
+    torch.save(opt.state_dict(), buf)
+    train(p, opt, 2)
+    for where in ("cuda", "cpu"):
+        buf.seek(0)
+        q, again = make()
+        q.data.copy_(start)
+        again.load_state_dict(torch.load(buf, map_location=where))
+        train(q, again, 2)
+        assert torch.equal(p, q) and again.param_groups[0]["lr"].item() == opt.param_groups[0]["lr"].item()
