@@ -687,3 +687,49 @@ def test_checkpoint_of_a_learning_rate_on_the_device(metis_lib):
         again.load_state_dict(torch.load(buf, map_location=where))
         train(q, again, 2)
         assert torch.equal(p, q) and again.param_groups[0]["lr"].item() == opt.param_groups[0]["lr"].item()
+
+
+@pytest.mark.parametrize("n", [6_000_077, 40_000_077])     # two and more state blocks a warp, and the most
+@pytest.mark.parametrize("rounding", ["rn", "sr"])
+@pytest.mark.parametrize("dtype,offset", [(torch.float32, 0), (torch.float32, 1), (torch.bfloat16, 0), (torch.bfloat16, 3)])
+def test_windows_of_long_tensors_match_the_oracle(metis_lib, n, rounding, dtype, offset):
+    """Windows at the start, across the borders of chunks and of the stretches that a warp takes, and at the ragged
+    end; gradients that differ by orders of magnitude from a state block to the next, and whose pattern moves with the
+    step, so that a block with its neighbour's exponent would show."""
+    from spectral_quantized_gemm_b200.optim import AdamW
+    g = torch.Generator(device="cuda").manual_seed(5)
+    p = torch.nn.Parameter(torch.randn(n + offset, device="cuda", generator=g).to(dtype)[offset:])
+    opt = AdamW([p], state_bits=8, rounding=rounding, seed=21, **HYPER)
+    rng = np.random.default_rng(n)
+    starts = [0, n // 128 * 128 - 1024, *(int(c) * 1024 - 1024 for c in rng.integers(1, n // 1024, 12)),
+              *(int(c) * 16384 - 1024 for c in rng.integers(1, n // 16384, 8))]
+    windows = [(a, min(a + 2048, n)) for a in starts]
+    states = [tuple((np.zeros(b - a, np.uint8), np.zeros(-(-(b - a) // 128), np.uint8)) for _ in range(2)) for a, b in windows]
+    block = torch.arange(n, device="cuda") // 128
+    (b1, b2), lr, eps, wd = HYPER["betas"], HYPER["lr"], HYPER["eps"], HYPER["weight_decay"]
+    for t in (1, 2, 3):
+        scale = 10.0 ** -((block * 5 + t) % 9).float()
+        p.grad = torch.empty(n + offset, dtype=dtype, device="cuda")[offset:].copy_(scale * torch.randn(n, device="cuda", generator=g))
+        before = [_np(p[a:b]) for a, b in windows]
+        opt.step()
+        s = opt.state[p]
+        for i, (a, b) in enumerate(windows):
+            grad = _np(p.grad[a:b])
+            m0, v0 = adamw.decode(*states[i][0], True), adamw.decode(*states[i][1], False)
+            m, v = adamw.moments(m0, v0, grad, b1, b2)
+            w = None
+            if rounding == "sr":
+                w = adamw.philox.stream_words(21, adamw.philox.tag(0, 4, 0), t, np.arange(a // 4, -(-b // 4), dtype=np.uint64))
+                w = w.reshape(-1)[:b - a]
+            new = (adamw.encode(m, True, None if w is None else w & np.uint64(0xFFFF)),
+                   adamw.encode(v, False, None if w is None else w >> np.uint64(16)))
+            for key, (codes, exponents) in zip(("exp_avg", "exp_avg_sq"), new):
+                assert np.array_equal(s[key][a:b].cpu().numpy(), codes), (t, a, key)
+                assert np.array_equal(s[key + "_exponent"][a // 128:-(-b // 128)].cpu().numpy(), exponents), (t, a, key)
+            states[i] = new
+            want = adamw.parameter(before[i], m, v, t, lr, b1, b2, eps, wd)
+            size = lr / (1 - b1 ** t) * (np.abs(b1 * m0) + np.abs((1 - b1) * grad)) / (np.sqrt(v) / math.sqrt(1 - b2 ** t) + eps)
+            bound = 3 * U * np.abs(before[i]) + 20 * U * size + 2.0 ** -148
+            if dtype == torch.bfloat16:
+                bound = bound + (2.0 ** -8 if rounding == "rn" else 2.0 ** -7) * (np.abs(want) + bound)
+            assert np.all(np.abs(_np(p[a:b]) - want) <= bound), (t, a)
