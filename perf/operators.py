@@ -204,15 +204,17 @@ def _prepare_adamw(case, s, gen):
     if not own:
         return
     from spectral_quantized_gemm_b200.optim import AdamW
-    params = [torch.nn.Parameter(s["p"][a:a + n].view(shape)) for a, n, shape in spans]
+    # the calls step the same elements as the plain form: a tensor's whole span of the flat buffers, the rest of
+    # its last BLOCK included, whose outputs are compared too
+    spans = [(a, a + -(-n // BLOCK) * BLOCK) for a, n, _ in spans]
+    params = [torch.nn.Parameter(s["p"][a:e]) for a, e in spans]
     opt = AdamW(params, lr=LR, betas=(BETA1, BETA2), eps=EPS, weight_decay=DECAY, state_bits=case["bits"],
                 rounding=case["rounding"], seed=_seed(case))
-    for p, (a, n, shape) in zip(params, spans):
-        p.grad = s["g"][a:a + n].view(shape)
-        st = {"step": s["step"], "exp_avg": s["m"][a:a + n].view(shape), "exp_avg_sq": s["v"][a:a + n].view(shape)}
+    for p, (a, e) in zip(params, spans):
+        p.grad = s["g"][a:e]
+        st = {"step": s["step"], "exp_avg": s["m"][a:e], "exp_avg_sq": s["v"][a:e]}
         if case["bits"] == 8:
-            b0, b1 = a // BLOCK, a // BLOCK + -(-n // BLOCK)
-            st["exp_avg_exponent"], st["exp_avg_sq_exponent"] = s["me"][b0:b1], s["ve"][b0:b1]
+            st["exp_avg_exponent"], st["exp_avg_sq_exponent"] = s["me"][a // BLOCK:e // BLOCK], s["ve"][a // BLOCK:e // BLOCK]
         opt.state[p] = st
     s["opt"] = opt
 
@@ -274,7 +276,6 @@ def _run_adamw(s):
     # the 8-bit states are returned as their whole numbers, codes and shared exponents: equal or not
     names = ("p", "m", "v", "me", "ve") if s["bits"] == 8 else ("p", "m", "v")
     if own:
-        _whole_spans(s)
         s["opt"].step()
         return {k: s[k] for k in names}
     s["step"] += 1
@@ -300,21 +301,6 @@ def _run_adamw(s):
         p = bits.view(torch.float32)
     s["p"] = p.to(_dtype(s["dtype"]))
     return {k: s[k] for k in names}
-
-
-def _whole_spans(s):
-    """The framework's calls step the same elements as the plain form: a tensor's whole span of the flat
-    buffers, the rest of its last BLOCK included, whose outputs are compared too."""
-    if "spans" in s:
-        return
-    group, at, s["spans"] = s["opt"].param_groups[0], 0, True
-    for i, shape in enumerate(_shapes(s)):
-        old, n = group["params"][i], -(-math.prod(shape) // BLOCK) * BLOCK
-        new, state = torch.nn.Parameter(s["p"][at:at + n]), s["opt"].state.pop(old)
-        new.grad = s["g"][at:at + n]
-        group["params"][i] = new
-        s["opt"].state[new] = dict(state, exp_avg=s["m"][at:at + n], exp_avg_sq=s["v"][at:at + n])
-        at += n
 
 
 def _power(k):
