@@ -457,9 +457,9 @@ struct View {
 
 // What a block has on its way in shared memory: each thread copies its own elements of the next two state
 // blocks here and reads them back, so nothing but the copies is waited for.  Only fp32 to nearest, which
-// waited for memory with one state block ahead in registers (71 M elements 220 us, 200 with the ring;
-// four or six stages 202, 209).  The others are bound by their instructions, and these are more: fp32
-// stochastic 238 us, 240 with it; bf16 301, 318 stochastic, 260, 274 to nearest.
+// waited for memory with one state block ahead in registers (71 M elements 246 us, 221 with the ring;
+// four or six stages 1% and 4% more).  The others do not gain: fp32 stochastic 261 us, 263 with it;
+// bf16 323, 341 stochastic, 301, 313 to nearest.
 template <typename T>
 struct Ring {
   static constexpr int STAGES = 3;
@@ -592,6 +592,12 @@ __device__ __forceinline__ bool run_chunk(const Table<CAP>& tab, int which, int6
   return bad;
 }
 
+// 8-bit states: 71 M elements, all with gradients, take 221 us (fp32 to nearest), 261 (fp32 stochastic), 301 and 323
+// (bf16).  Elements without gradients may settle on a border -- beta2 = 0.95 takes a v of code 10 to 9.5, and the
+// nearest code is 10 again -- where the fp64 route decides in every step: with 2% of those 305 and 330 to nearest.
+// Three blocks an SM leave 80 registers a thread, of which 4 to 12 bytes spill to nearest and 60 (bf16) or 76
+// (fp32) with the words of the stochastic rounding; four blocks, or blocks of 128 threads at 5 to 7 an SM,
+// were not faster.  Neither the issue slots (62%) nor the integer pipe (61%) nor HBM (39%) is full.
 template <typename T, int BITS, bool SR, int CAP>
 __global__ void __launch_bounds__(kThreads, BITS == 32 ? 5 : 3) adamw_kernel(const __grid_constant__ Table<CAP> tab) {
   __shared__ Step sh;

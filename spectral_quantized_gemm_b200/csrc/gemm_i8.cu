@@ -19,8 +19,8 @@
 // gemm_i8_pair_kernel: large products.  A cluster of two CTAs computes 256 x 256 tiles with
 // cta_group::2 MMAs (each CTA loads 128 rows of A and 128 of B for every 128 K elements),
 // persistent over the tiles, with two accumulators so that the epilogue of a tile runs
-// under the MMAs of the next.  8192 x 4096 x 14336 takes 325 us by itself, with the tensor pipe busy 81%
-// of the time.
+// under the MMAs of the next.  8192 x 4096 x 14336 takes 345 us in a row of others like it, at the power limit;
+// a launch alone under the profiler took 325 with the tensor pipe busy 81% of the time.
 //
 // Every mbarrier wait is bounded; on expiry the CTA raises METIS_DEV_TIMEOUT, stops
 // issuing work and exits after releasing its tensor memory.

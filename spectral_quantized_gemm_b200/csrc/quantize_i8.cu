@@ -207,7 +207,7 @@ __device__ __forceinline__ void store_codes(int8_t* row, int c, int cols, uint2 
 // and the codes, so it is read once; the next row is loaded before the work on one begins
 // (without that a block waited for its loads most of the time, 2 us more at 8192 x 4096 bf16).
 // A block is one group, or eight where a group is a warp, and goes on to further rows.  8192 x 4096 bf16
-// takes 15.9 us, 6.3 TB/s of elements and codes; 4096 x 14336 fp32 48.5, 6.0.
+// takes 17 us, 5.9 TB/s of elements and codes; 4096 x 14336 fp32 47.4, 6.2.
 //   TOPS: a thread meets the same columns in every row; it keeps their maxima in shared memory
 // (its own words, 64 registers a thread are full), and the block joins them into one of kCopies
 // copies of `tops` by integer atomicMax, whose order does not matter.  Many copies and few blocks,
@@ -392,8 +392,8 @@ __global__ void __launch_bounds__(512) quantize_i8_long_rows_kernel(const T* __r
 // consecutive rows, so its codes are 16 bytes of a column each; the lanes of a warp are 4 words
 // by 8 such pieces, so a column leaves as 128 bytes.  16 bytes of padding after 16 rows keep
 // the pieces on different banks.  Tiles go from the last row to the first: the last rows read
-// before are what L2 still holds.  With the rows' pass 8192 x 4096 bf16 takes 40 us, 4096 x 14336 fp32 107:
-// two readings, and 60% of the issue slots.
+// before are what L2 still holds.  With the rows' pass 8192 x 4096 bf16 takes 38.5 us, 4096 x 14336 fp32 108
+// (34 and 88 where only columns are asked for): two readings, and 60% of the issue slots.
 //   (One reading instead of two, by clusters that keep strips of columns in shared memory while
 // their maxima are joined, took 36 us or more at 8192 x 4096 bf16 in all forms tried: a block
 // waited most of its time for the join.)
@@ -556,8 +556,8 @@ cudaError_t run_quantize(const T* M, int64_t rows, int64_t cols, int64_t ld, con
                         col->scales, (const uint32_t*)tops, (const uint32_t*)marks);
   };
   // Rows of a tile: 256, or half that where there would be fewer than two blocks for an SM.  Both
-  // orientations, 128 against 256: 1001 x 1333 bf16 9.6 us, 14.2; 512 x 2304 8.6, 10.3; 2048 x 2048 11.2,
-  // 11.9; 4096 x 2048 15.5, 14.9; 8192 x 4096 47.7, 42.8.
+  // orientations, 128 against 256: 1001 x 1333 bf16 10.3 us, 13.0; 2048 x 2048 10.0, 10.4; 4096 x 2048 14.3,
+  // 13.8; 8192 x 4096 42.9, 38.5.
   if (strips * ((rows + 255) / 256) < 2 * (int64_t)sm_count) return launch(quantize_i8_cols_kernel<T, 128>, 128);
   return launch(quantize_i8_cols_kernel<T, 256>, 256);
 }
